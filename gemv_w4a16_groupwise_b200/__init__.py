@@ -17,6 +17,13 @@ Entry points (same names as the C ABI in ``include/w4a16.h``):
   products on the tensor pipe, fp32 sums)
 * :func:`w4_gather_columns` / :func:`w4_scatter_columns` -- the column
   permutations of act-order weights (``perm=`` on the calls above)
+* :func:`w8_quantize_rows` -- bf16 rows -> int8 codes and one fp32 scale per row
+* :func:`w8a8_gemm` -- the product of int8 tokens and int8 weights with a scale
+  for each token and channel, forward (optional bias) and transposed
+* :func:`w8a8_linear` -- both on bf16 rows in one call
+* :func:`w4_block_norm` / :func:`w4_block_norm_backward` -- the norms before and
+  after a block fused with its gate, residual scale and residual add, as bf16 or
+  as int8 rows for the products above
 * :func:`w4_workspace_bytes`, :func:`w4_device_error`
 
 :mod:`gemv_w4a16_groupwise_b200.tp` shards one layer over torch.distributed
@@ -30,6 +37,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import Any, NamedTuple
 
 from . import build as _build
 
@@ -95,6 +103,23 @@ def library():
             lib.w4_scatter_columns.restype = I
             lib.w4_invert_permutation.argtypes = [P, I, P, P]
             lib.w4_invert_permutation.restype = I
+            L, F = ctypes.c_longlong, ctypes.c_float
+            lib.w8_quantize_rows.argtypes = [P, I, I, P, P, L, P, P]
+            lib.w8_quantize_rows.restype = I
+            for name in ("w8a8_workspace_bytes", "w8a8_linear_workspace_bytes"):
+                f = getattr(lib, name)
+                f.argtypes = [I, I, I, I]
+                f.restype = Z
+            lib.w8a8_gemm.argtypes = [P, L, P, I, I, I, P, L, P, P, I, P, P, Z, P]
+            lib.w8a8_gemm.restype = I
+            lib.w8a8_linear.argtypes = [P, I, I, I, P, L, P, P, I, P, P, Z, P]
+            lib.w8a8_linear.restype = I
+            lib.w4_block_norm.argtypes = [P, P, I, I, P, P, I, F, P, F, F, P, P, L, P, P, P]
+            lib.w4_block_norm.restype = I
+            lib.w4_block_norm_workspace_bytes.argtypes = [I, I]
+            lib.w4_block_norm_workspace_bytes.restype = Z
+            lib.w4_block_norm_backward.argtypes = [P, P, P, P, P, I, I, P, P, I, F, P, F, P, P, P, P, P, P, Z, P]
+            lib.w4_block_norm_backward.restype = I
             _lib = lib
     return _lib
 
@@ -385,6 +410,266 @@ def w4_scatter_columns(A, idx, dst_cols: int, out=None):
     if st != 0:
         raise W4Error(st, "w4_scatter_columns")
     return out
+
+
+def _check_on(dev, *named):
+    """The other tensors of a call live where the first one does."""
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _check_codes(t, name, rows=None, cols=None) -> int:
+    """Check int8 rows and return their stride in bytes, a multiple of 16 that
+    covers a row rounded up to 16 (the layout :func:`w8_quantize_rows` gives)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device (no CPU path exists)")
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be {torch.int8}, got {t.dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    R, C = t.shape
+    need = (C + 15) // 16 * 16
+    ld = t.stride(0) if R > 1 else need
+    if (C > 1 and t.stride(1) != 1) or ld % 16 or ld < need:
+        raise ValueError(f"{name}: rows must be dense and start every multiple of 16 bytes, got strides {t.stride()}")
+    if R and t.untyped_storage().nbytes() < t.storage_offset() + (R - 1) * ld + need:
+        raise ValueError(f"{name}: the last row must be readable up to a multiple of 16 bytes")
+    return ld
+
+
+def _empty_codes(R: int, C: int, dev):
+    torch = _torch()
+    C16 = (C + 15) // 16 * 16
+    q = torch.empty((R, C16), dtype=torch.int8, device=dev)
+    return q if C16 == C else q[:, :C]
+
+
+def w8_quantize_rows(X, channel_scales=None, out=None):
+    """int8 codes and one fp32 scale per row of bf16 X [R, C]: scales = max|v| / 127,
+    codes = rint(127 v / max|v|), v = X, or X * channel_scales (fp32 [C]).
+
+    The codes' rows start every multiple of 16 bytes (a view of a wider tensor
+    when C is not one).  A row of zeros has scale 0, a row with an infinity or a
+    NaN scale NaN and codes 0.  ``out``: (codes, scales) to write into."""
+    torch = _torch()
+    _check_cuda(X, "X", torch.bfloat16)
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    R, C = X.shape
+    dev = X.device
+    if channel_scales is not None:
+        _check_cuda(channel_scales, "channel_scales", torch.float32, (C,))
+    if out is None:
+        codes, scales = _empty_codes(R, C, dev), torch.empty((R,), dtype=torch.float32, device=dev)
+        ld = (C + 15) // 16 * 16
+    else:
+        codes, scales = out
+        ld = _check_codes(codes, "codes", R, C)
+        _check_cuda(scales, "scales", torch.float32, (R,))
+    _check_on(dev, ("channel_scales", channel_scales), ("codes", codes), ("scales", scales))
+    with _OnDevice(dev) as on:
+        st = library().w8_quantize_rows(X.data_ptr(), R, C,
+                                        None if channel_scales is None else channel_scales.data_ptr(),
+                                        codes.data_ptr(), ld, scales.data_ptr(), _stream_ptr(on.idx))
+    if st != 0:
+        raise W4Error(st, "w8_quantize_rows")
+    return codes, scales
+
+
+def _w8_product(fname, A, a_scales, lda, codes, scales, bias, transposed, out):
+    torch = _torch()
+    ldw = _check_codes(codes, "codes")
+    N, K = codes.shape
+    in_len, out_len = (N, K) if transposed else (K, N)
+    if A.dim() != 2 or A.shape[1] != in_len:
+        raise ValueError(f"A must be 2-D with {in_len} columns, got {tuple(A.shape)}")
+    M = A.shape[0]
+    dev = A.device
+    if scales is not None:
+        _check_cuda(scales, "scales", torch.float32, (N,))
+    if a_scales is not None:
+        _check_cuda(a_scales, "a_scales", torch.float32, (M,))
+    if bias is not None:
+        _check_cuda(bias, "bias", torch.bfloat16, (out_len,))
+    if out is None:
+        out = torch.empty((M, out_len), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_cuda(out, "out", torch.bfloat16, (M, out_len))
+    _check_on(dev, ("codes", codes), ("scales", scales), ("a_scales", a_scales), ("bias", bias), ("out", out))
+    lib = library()
+    with _OnDevice(dev) as on:
+        key = (fname, on.idx, M, N, K, bool(transposed))
+        nws = _ws_cache.get(key)
+        if nws is None:
+            nws = int(getattr(lib, "w8a8_linear_workspace_bytes" if lda is None else "w8a8_workspace_bytes")(
+                M, N, K, int(bool(transposed))))
+            if len(_ws_cache) > 4096:
+                _ws_cache.clear()
+            _ws_cache[key] = nws
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+        head = (A.data_ptr(),) if lda is None else (A.data_ptr(), lda, a_scales.data_ptr())
+        st = getattr(lib, fname)(
+            *head, M, N, K, codes.data_ptr(), ldw, None if scales is None else scales.data_ptr(),
+            None if bias is None else bias.data_ptr(), int(bool(transposed)), out.data_ptr(),
+            None if ws is None else ws.data_ptr(), nws, _stream_ptr(on.idx))
+    if st != 0:
+        raise W4Error(st, fname)
+    return out
+
+
+def w8a8_gemm(A, a_scales, codes, scales=None, *, bias=None, transposed: bool = False, out=None):
+    """Product of int8 tokens A with int8 weights ``codes`` [N, K], exact integer sums:
+
+    Y[m, n] = a_scales[m] scales[n] sum_k A[m, k] codes[n, k] + bias[n], or, transposed,
+    dX[m, k] = a_scales[m] sum_n A[m, n] codes[n, k] + bias[k], where A holds the rows of
+    dY quantized with ``channel_scales=scales`` and ``scales`` is left out here.
+    bf16 output; ``out`` may not overlap the inputs."""
+    if transposed and scales is not None:
+        raise ValueError("transposed: fold the weights' scales into A "
+                         "(w8_quantize_rows with channel_scales) and pass scales=None")
+    if not transposed and scales is None:
+        raise ValueError("scales of the weights are needed")
+    if a_scales is None:
+        raise ValueError("a_scales are needed")
+    lda = _check_codes(A, "A")
+    return _w8_product("w8a8_gemm", A, a_scales, lda, codes, scales, bias, transposed, out)
+
+
+def w8a8_linear(A, codes, scales, *, bias=None, transposed: bool = False, out=None):
+    """8-bit linear layer on bf16 rows: :func:`w8_quantize_rows` on A and
+    :func:`w8a8_gemm` in one call.  Y = A . dequant(codes)^T (A [M, K]), or,
+    transposed, dX = A . dequant(codes) (A [M, N]).  ``out`` may not overlap the inputs."""
+    _check_cuda(A, "A", _torch().bfloat16)
+    if scales is None:
+        raise ValueError("scales of the weights are needed")
+    return _w8_product("w8a8_linear", A, None, None, codes, scales, bias, transposed, out)
+
+
+class BlockNorm(NamedTuple):
+    """What :func:`w4_block_norm` gives; fields that were not asked for are None."""
+    residual: Any       # bf16 [M, C]
+    normed: Any         # bf16 [M, C], or int8 codes
+    scales: Any         # fp32 [M], of the codes
+    rstd: Any           # fp32 [2, M], for the backward pass
+
+
+class BlockNormGrad(NamedTuple):
+    """Gradients of :func:`w4_block_norm`; None where the forward had no such input."""
+    d_x: Any
+    d_y: Any
+    d_pre_weight: Any
+    d_post_weight: Any
+    d_gate: Any
+
+
+def _check_norm(rows, C, dev, pre_weight, post_weight, gate, y):
+    """The norm's weights and gate; returns the C API's gate kind."""
+    torch = _torch()
+    _check_cuda(pre_weight, "pre_weight", torch.bfloat16, (C,))
+    if y is None and (post_weight is not None or gate is not None):
+        raise ValueError("post_weight and gate belong to y, which is not given")
+    if post_weight is not None:
+        _check_cuda(post_weight, "post_weight", torch.bfloat16, (C,))
+    kind = 0
+    if gate is not None:
+        kind = 1 if isinstance(gate, torch.Tensor) and gate.dim() == 1 else 2
+        _check_cuda(gate, "gate", torch.bfloat16, (C,) if kind == 1 else (rows, C))
+    _check_on(dev, ("pre_weight", pre_weight), ("post_weight", post_weight), ("gate", gate))
+    return kind
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def w4_block_norm(x, y=None, *, pre_weight, post_weight=None, gate=None, residual_scale: float = 1.0,
+                  weight_offset: float = 0.0, eps: float = 1e-5, quantize: bool = False,
+                  keep_rstd: bool = False, residual_out=None) -> BlockNorm:
+    """residual = x + residual_scale * gate * norm(y; post_weight), then norm(residual; pre_weight).
+
+    x, y: bf16 [M, C], C <= 16384; y is the output of the block before (None: there is
+    none, and x itself is normed and returned as the residual).  post_weight (bf16 [C])
+    is the norm after that block, pre_weight the one before the next; weights are
+    w + weight_offset.  gate: bf16 [C] or [M, C].  ``quantize`` gives the normed rows as
+    int8 codes and scales for :func:`w8a8_gemm` instead of bf16.  ``keep_rstd`` keeps what
+    :func:`w4_block_norm_backward` needs.  ``residual_out`` may be x or y (in place)."""
+    torch = _torch()
+    _check_cuda(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    M, C = x.shape
+    dev = x.device
+    if y is not None:
+        _check_cuda(y, "y", torch.bfloat16, (M, C))
+    elif residual_out is not None:
+        raise ValueError("without y the residual is x itself")
+    kind = _check_norm(M, C, dev, pre_weight, post_weight, gate, y)
+    residual = x
+    if y is not None:
+        if residual_out is None:
+            residual = torch.empty_like(x)
+        else:
+            _check_cuda(residual_out, "residual_out", torch.bfloat16, (M, C))
+            residual = residual_out
+    _check_on(dev, ("y", y), ("residual_out", residual))
+    scales = None
+    if quantize:
+        normed, scales = _empty_codes(M, C, dev), torch.empty((M,), dtype=torch.float32, device=dev)
+    else:
+        normed = torch.empty((M, C), dtype=torch.bfloat16, device=dev)
+    rstd = torch.empty((2, M), dtype=torch.float32, device=dev) if keep_rstd else None
+    with _OnDevice(dev) as on:
+        st = library().w4_block_norm(
+            x.data_ptr(), _ptr(y), M, C, _ptr(post_weight), _ptr(gate), kind, residual_scale,
+            pre_weight.data_ptr(), weight_offset, eps, None if y is None else residual.data_ptr(),
+            normed.data_ptr(), (C + 15) // 16 * 16, _ptr(scales), _ptr(rstd), _stream_ptr(on.idx))
+    if st != 0:
+        raise W4Error(st, "w4_block_norm")
+    return BlockNorm(residual, normed, scales, rstd)
+
+
+def w4_block_norm_backward(d_normed, residual, rstd, y=None, *, d_residual=None, pre_weight, post_weight=None,
+                           gate=None, residual_scale: float = 1.0, weight_offset: float = 0.0) -> BlockNormGrad:
+    """Gradients of :func:`w4_block_norm` from d_normed and d_residual (None: zero), with
+    the residual and rstd that it returned (``keep_rstd=True``), its y, weights and gate.
+
+    All bf16: d_x, d_y [M, C], d_pre_weight, d_post_weight [C], d_gate in the gate's shape.
+    Quantized rows count as the values they stand for.  The same inputs give the same bits."""
+    torch = _torch()
+    _check_cuda(d_normed, "d_normed", torch.bfloat16)
+    if d_normed.dim() != 2:
+        raise ValueError("d_normed must be 2-D")
+    M, C = d_normed.shape
+    dev = d_normed.device
+    _check_cuda(residual, "residual", torch.bfloat16, (M, C))
+    _check_cuda(rstd, "rstd", torch.float32, (2, M))
+    if d_residual is not None:
+        _check_cuda(d_residual, "d_residual", torch.bfloat16, (M, C))
+    if y is not None:
+        _check_cuda(y, "y", torch.bfloat16, (M, C))
+    kind = _check_norm(M, C, dev, pre_weight, post_weight, gate, y)
+    _check_on(dev, ("residual", residual), ("rstd", rstd), ("d_residual", d_residual), ("y", y))
+    d_x = torch.empty_like(d_normed)
+    d_y = None if y is None else torch.empty_like(y)
+    d_pre = torch.empty_like(pre_weight)
+    d_post = None if post_weight is None else torch.empty_like(post_weight)
+    d_gate = None if gate is None else torch.empty_like(gate)
+    lib = library()
+    with _OnDevice(dev) as on:
+        nws = int(lib.w4_block_norm_workspace_bytes(M, C))
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+        st = lib.w4_block_norm_backward(
+            d_normed.data_ptr(), _ptr(d_residual), residual.data_ptr(), rstd.data_ptr(), _ptr(y), M, C,
+            _ptr(post_weight), _ptr(gate), kind, residual_scale, pre_weight.data_ptr(), weight_offset,
+            d_x.data_ptr(), _ptr(d_y), d_pre.data_ptr(), _ptr(d_post), _ptr(d_gate), ws.data_ptr(), nws,
+            _stream_ptr(on.idx))
+    if st != 0:
+        raise W4Error(st, "w4_block_norm_backward")
+    return BlockNormGrad(d_x, d_y, d_pre, d_post, d_gate)
 
 
 def w4_launch_count() -> int:

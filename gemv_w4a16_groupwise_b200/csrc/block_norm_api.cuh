@@ -1,0 +1,146 @@
+// C-ABI entry points of the block norms: validation and dispatch.  Included
+// by w4a16.cu, whose host helpers it uses.
+#pragma once
+
+namespace {
+
+// The block of a row of C: the fewest threads that hold it in one vector of
+// 8 each, up to 512, then two vectors each.
+template <template <int, int, int> class Launch, typename... Args>
+w4_status dispatch_row(int C, Args... args) {
+    const bool vec = C % 8 == 0;
+    if (C <= 1024) return vec ? Launch<128, 1, 8>::run(args...) : Launch<128, 8, 1>::run(args...);
+    if (C <= 2048) return vec ? Launch<256, 1, 8>::run(args...) : Launch<256, 8, 1>::run(args...);
+    if (C <= 4096) return vec ? Launch<256, 2, 8>::run(args...) : Launch<256, 16, 1>::run(args...);
+    if (C <= 8192) return vec ? Launch<512, 2, 8>::run(args...) : Launch<512, 16, 1>::run(args...);
+    return vec ? Launch<1024, 2, 8>::run(args...) : Launch<1024, 16, 1>::run(args...);
+}
+
+template <int T, int V, int VEC>
+struct NormLaunch {
+    static w4_status run(const w4::NormArgs& a, cudaStream_t st) {
+        if (a.scales) launch_pdl(w4::block_norm_kernel<T, V, VEC, true>, dim3(a.M), dim3(T), 0, st, a);
+        else launch_pdl(w4::block_norm_kernel<T, V, VEC, false>, dim3(a.M), dim3(T), 0, st, a);
+        return launch_status();
+    }
+};
+
+// Blocks of the backward pass: two per SM (each leaves a partial row of the
+// weight gradients), one of 1024 threads.
+int norm_grad_blocks(int M, int C, int sms) { return std::min(M, C > 8192 ? sms : 2 * sms); }
+
+template <int T, int V, int VEC>
+struct NormGradLaunch {
+    static w4_status run(const w4::NormGradArgs& a, int blocks, int sums, cudaStream_t st) {
+        constexpr bool kSmem = T == 1024;
+        const size_t smem = kSmem ? static_cast<size_t>(sums) * T * V * VEC * sizeof(float) : 0;
+        auto fn = w4::block_norm_backward_kernel<T, V, VEC, kSmem>;
+        if (smem > 48 * 1024 && ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
+        launch_pdl(fn, dim3(blocks), dim3(T), smem, st, a);
+        return launch_status();
+    }
+};
+
+bool gate_ok(int gate_kind, const void* gate, const void* y) {
+    if (gate_kind < W4_GATE_NONE || gate_kind > W4_GATE_TOKEN) return false;
+    return (gate != nullptr) == (gate_kind != W4_GATE_NONE) && (y || !gate);
+}
+
+}  // namespace
+
+extern "C" {
+
+w4_status w4_block_norm(const void* x, const void* y, int M, int C, const void* post_weight, const void* gate,
+                        int gate_kind, float residual_scale, const void* pre_weight, float weight_offset, float eps,
+                        void* residual, void* normed, long long ld, float* scales, float* rstd, void* stream) {
+    if (M <= 0 || C <= 0) return W4_ERR_INVALID_ARG;
+    if (C > w4::kNormMaxC) return W4_ERR_UNSUPPORTED;
+    if (!gate_ok(gate_kind, gate, y) || !(eps > 0.0f) || !(eps < 3.4e38f)) return W4_ERR_INVALID_ARG;
+    if (!x || !pre_weight || !normed || (post_weight && !y) || (residual != nullptr) != (y != nullptr))
+        return W4_ERR_INVALID_ARG;
+    if (scales && ld < C) return W4_ERR_INVALID_ARG;
+    for (const void* p : {x, y, post_weight, gate, pre_weight, static_cast<const void*>(residual),
+                          static_cast<const void*>(normed), static_cast<const void*>(scales),
+                          static_cast<const void*>(rstd)})
+        if (!aligned16(p)) return W4_ERR_ALIGNMENT;
+    if (scales && ld % 16 != 0) return W4_ERR_ALIGNMENT;
+    w4::NormArgs a;
+    a.x = static_cast<const uint16_t*>(x);
+    a.y = static_cast<const uint16_t*>(y);
+    a.post = static_cast<const uint16_t*>(post_weight);
+    a.gate = static_cast<const uint16_t*>(gate);
+    a.pre = static_cast<const uint16_t*>(pre_weight);
+    a.residual = static_cast<uint16_t*>(residual);
+    a.normed = normed;
+    a.scales = scales;
+    a.rstd = rstd;
+    a.M = M;
+    a.C = C;
+    a.gate_kind = gate_kind;
+    a.ld = ld;
+    a.alpha = residual_scale;
+    a.off = weight_offset;
+    a.eps = eps;
+    return dispatch_row<NormLaunch>(C, a, static_cast<cudaStream_t>(stream));
+}
+
+size_t w4_block_norm_workspace_bytes(int M, int C) {
+    if (M <= 0 || C <= 0) return 0;
+    const int blocks = norm_grad_blocks(M, C, device_info(current_device()).sms);
+    return static_cast<size_t>(3) * blocks * C * sizeof(float);
+}
+
+w4_status w4_block_norm_backward(const void* d_normed, const void* d_residual, const void* residual,
+                                 const float* rstd, const void* y, int M, int C, const void* post_weight,
+                                 const void* gate, int gate_kind, float residual_scale, const void* pre_weight,
+                                 float weight_offset, void* d_x, void* d_y, void* d_pre_weight, void* d_post_weight,
+                                 void* d_gate, void* workspace, size_t workspace_bytes, void* stream) {
+    if (M <= 0 || C <= 0) return W4_ERR_INVALID_ARG;
+    if (C > w4::kNormMaxC) return W4_ERR_UNSUPPORTED;
+    if (!gate_ok(gate_kind, gate, y)) return W4_ERR_INVALID_ARG;
+    if (!d_normed || !residual || !rstd || !pre_weight || !d_x || !d_pre_weight || (post_weight && !y))
+        return W4_ERR_INVALID_ARG;
+    if ((d_y != nullptr) != (y != nullptr) || (d_post_weight != nullptr) != (post_weight != nullptr) ||
+        (d_gate != nullptr) != (gate != nullptr))
+        return W4_ERR_INVALID_ARG;
+    for (const void* p : {d_normed, d_residual, residual, static_cast<const void*>(rstd), y, post_weight, gate,
+                          pre_weight, static_cast<const void*>(d_x), static_cast<const void*>(d_y),
+                          static_cast<const void*>(d_pre_weight), static_cast<const void*>(d_post_weight),
+                          static_cast<const void*>(d_gate), static_cast<const void*>(workspace)})
+        if (!aligned16(p)) return W4_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < w4_block_norm_workspace_bytes(M, C)) return W4_ERR_WORKSPACE;
+    const bool chan = gate_kind == W4_GATE_CHANNEL;
+    w4::NormGradArgs a;
+    a.dn = static_cast<const uint16_t*>(d_normed);
+    a.dres = static_cast<const uint16_t*>(d_residual);
+    a.r = static_cast<const uint16_t*>(residual);
+    a.rstd = rstd;
+    a.y = static_cast<const uint16_t*>(y);
+    a.post = static_cast<const uint16_t*>(post_weight);
+    a.gate = static_cast<const uint16_t*>(gate);
+    a.pre = static_cast<const uint16_t*>(pre_weight);
+    a.dx = static_cast<uint16_t*>(d_x);
+    a.dy = static_cast<uint16_t*>(d_y);
+    a.dgate_token = chan ? nullptr : static_cast<uint16_t*>(d_gate);
+    a.part = static_cast<float*>(workspace);
+    a.M = M;
+    a.C = C;
+    a.gate_kind = gate_kind;
+    a.alpha = residual_scale;
+    a.off = weight_offset;
+    const int blocks = norm_grad_blocks(M, C, device_info(current_device()).sms);
+    const int sums = 1 + (post_weight ? 1 : 0) + (chan ? 1 : 0);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const w4_status s = dispatch_row<NormGradLaunch>(C, a, blocks, sums, st);
+    if (s != W4_OK) return s;
+    // the slabs in order: pre, post, gate
+    uint16_t* o[3] = {static_cast<uint16_t*>(d_pre_weight), nullptr, nullptr};
+    int k = 1;
+    if (post_weight) o[k++] = static_cast<uint16_t*>(d_post_weight);
+    if (chan) o[k++] = static_cast<uint16_t*>(d_gate);
+    launch_pdl(w4::column_sums_kernel, dim3((C + 31) / 32, sums), dim3(256), 0, st,
+               static_cast<const float*>(a.part), blocks, C, o[0], o[1], o[2]);
+    return launch_status();
+}
+
+}  // extern "C"

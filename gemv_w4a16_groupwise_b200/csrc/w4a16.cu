@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "block_norm.cuh"
 #include "common.cuh"
 #include "gemm_simple.cuh"
 #include "gemm_tc.cuh"
@@ -19,6 +20,8 @@
 #include "permute.cuh"
 #include "quantize.cuh"
 #include "w4a16.h"
+#include "w8_gemm.cuh"
+#include "w8_quantize.cuh"
 
 namespace {
 
@@ -1286,3 +1289,6 @@ w4_status w4_scatter_columns(const void* A, int M, int L, const int32_t* idx, in
 }
 
 }  // extern "C"
+
+#include "w8_api.cuh"
+#include "block_norm_api.cuh"

@@ -1,5 +1,6 @@
 /*
- * w4a16.h -- C ABI of the B200 (sm_100a) weight-only int4 matmul library.
+ * w4a16.h -- C ABI of the B200 (sm_100a) weight-only int4 matmul library,
+ * with an 8-bit integer layer and the norms around a block beside it.
  *
  * The operation: Y = X_bf16 . dequant(W_int4)^T, where each 4-bit code q
  * of W carries a per-group fp16 scale s and zero point z and dequantizes as
@@ -207,6 +208,112 @@ w4_status w4_scatter_columns(const void *A, int M, int L, const int32_t *idx, in
  * the gather by inv, whose writes are contiguous.  Asynchronous on `stream`.
  */
 w4_status w4_invert_permutation(const int32_t *perm, int n, int32_t *inv, void *stream);
+
+/*
+ * 8-bit integers.  The same layer with int8 weights and int8 tokens: one fp32
+ * scale per weight row (channel) and one per token row, as in the scaled
+ * product that vLLM "Adding bias epilogue support for cutlass_scaled_mm" adds
+ * its bias epilogue to.  Codes are int8 rows, `ld` bytes apart, ld a multiple
+ * of 16 and at least the row length rounded up to 16 (so that rows start on 16
+ * bytes and may be read in 16-byte pieces; what lies behind the row length is
+ * never used).  Scales are fp32.
+ *
+ * w8_quantize_rows -- rows of bf16 X [R, C], or of X[r, c] * channel_scales[c]
+ * (fp32 [C], or NULL), as int8 codes with one scale per row:
+ *     scales[r] = fp32(max|v| / 127),   codes = rint(127 v / max|v|)
+ * symmetric, round half to even; for bf16 v the codes are those of the exact
+ * quotient (products with channel_scales are rounded to fp32 first).  A row of
+ * zeros has scale 0 and codes 0; a row with an infinity or a NaN has scale NaN
+ * and codes 0, so that everything it takes part in is NaN.  Used on weights
+ * (rows = channels), on tokens, and, with channel_scales = the weights' scales,
+ * on the gradients dY of the transposed product.
+ * Validation: R, C > 0; ld >= C; X, codes, scales non-NULL (W4_ERR_INVALID_ARG);
+ * pointers 16-byte aligned and ld a multiple of 16 (W4_ERR_ALIGNMENT).
+ */
+w4_status w8_quantize_rows(const void *X, int R, int C, const float *channel_scales, int8_t *codes,
+                           long long ld, float *scales, void *stream);
+
+/* Workspace bytes of w8a8_gemm and of w8a8_linear for this problem. */
+size_t w8a8_workspace_bytes(int M, int N, int K, int transposed);
+size_t w8a8_linear_workspace_bytes(int M, int N, int K, int transposed);
+
+/*
+ * w8a8_gemm -- product of int8 tokens and int8 weights W [N, K].
+ *   transposed = 0:  A [M, K] -> Y [M, N]:
+ *       Y[m, n] = bf16(a_scales[m] w_scales[n] sum_k A[m, k] W[n, k] + bias[n])
+ *   transposed = 1:  A [M, N] -> Y [M, K], the backward product from the same
+ *       weights; their scales lie along the sum, so A holds the codes of
+ *       dY * w_scales (w8_quantize_rows with channel_scales) and w_scales must
+ *       be NULL:
+ *       Y[m, k] = bf16(a_scales[m] sum_n A[m, n] W[n, k] + bias[k])
+ * The integer sums are exact; scales and bias are applied in fp32 and rounded
+ * once.  bias: bf16 over the output columns, or NULL.  Any codes of int8 are
+ * taken, -128 included.
+ * Validation: M, N, K > 0; lda, ldw >= their row lengths; pointers non-NULL
+ * (bias may be NULL, w_scales as above); the length of the sum (K, transposed
+ * N) at most 131071, beyond which int32 could overflow (W4_ERR_UNSUPPORTED);
+ * pointers 16-byte aligned, lda and ldw multiples of 16 (W4_ERR_ALIGNMENT);
+ * workspace_bytes >= w8a8_workspace_bytes (W4_ERR_WORKSPACE).
+ */
+w4_status w8a8_gemm(const int8_t *A, long long lda, const float *a_scales, int M, int N, int K,
+                    const int8_t *W, long long ldw, const float *w_scales, const void *bias, int transposed,
+                    void *Y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * w8a8_linear -- w8_quantize_rows on bf16 A and w8a8_gemm on its codes in one
+ * call: Y = A . dequant(W)^T (A [M, K]) or, transposed, dX = A . dequant(W)
+ * (A = dY [M, N]; w_scales is folded into the rows before they are quantized).
+ * w_scales is needed in both directions.  Validation as for w8a8_gemm.
+ */
+w4_status w8a8_linear(const void *A, int M, int N, int K, const int8_t *W, long long ldw,
+                      const float *w_scales, const void *bias, int transposed, void *Y, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * Norms around a block, fused with the residual add between them.  With
+ * norm(v) = v / sqrt(mean(v^2) + eps) over a row of C:
+ *     t = y;  t = norm(y) * (post_weight + weight_offset);  t = t * gate
+ *     residual = bf16(x + residual_scale * t)
+ *     normed   = norm(residual) * (pre_weight + weight_offset)
+ * post_weight (the norm after the block) and gate may be left out; `normed`
+ * reads the residual as it is stored.  normed is bf16 [M, C], or, when `scales`
+ * is given, int8 codes (row stride ld) with one scale per row, quantized from
+ * fp32 as by w8_quantize_rows: the input of w8a8_gemm.  Without y (the first
+ * block) post_weight, gate and residual must be NULL and x itself is normed.
+ * rstd: fp32 [2, M], or NULL: 1 / sqrt(mean + eps) of the norm after the block
+ * (0 without one) and of the norm before the next, which the backward pass
+ * takes.  residual may be x or y (in place).
+ *   gate_kind: W4_GATE_NONE, W4_GATE_CHANNEL (bf16 [C]), W4_GATE_TOKEN (bf16 [M, C]).
+ * All rows are bf16, dense.  Statistics are fp32.
+ * Validation: M, C > 0; C <= 16384 (W4_ERR_UNSUPPORTED); gate_kind in range;
+ * eps > 0 and finite; x, pre_weight, normed non-NULL; residual non-NULL exactly
+ * when y is; with scales ld >= C; pointers (and ld) 16-byte aligned.
+ */
+enum { W4_GATE_NONE = 0, W4_GATE_CHANNEL = 1, W4_GATE_TOKEN = 2 };
+
+w4_status w4_block_norm(const void *x, const void *y, int M, int C, const void *post_weight, const void *gate,
+                        int gate_kind, float residual_scale, const void *pre_weight, float weight_offset,
+                        float eps, void *residual, void *normed, long long ld, float *scales, float *rstd,
+                        void *stream);
+
+/*
+ * w4_block_norm_backward -- gradients of w4_block_norm from the gradients of
+ * its outputs (d_residual may be NULL: none; codes count as the values they
+ * stand for) and from residual, rstd and y.  Writes bf16: d_x [M, C]; with y:
+ * d_y [M, C], d_post_weight [C] with a post_weight, d_gate ([C] or [M, C]) with
+ * a gate; d_pre_weight [C].  Sums over the rows are fp32 in a fixed order.
+ * Without y: d_x and d_pre_weight.
+ * Outputs may not overlap inputs, except d_x = d_residual or d_normed, and d_y = y.
+ * Validation as for w4_block_norm; workspace_bytes >=
+ * w4_block_norm_workspace_bytes(M, C), a workspace that is 16-byte aligned.
+ */
+size_t w4_block_norm_workspace_bytes(int M, int C);
+w4_status w4_block_norm_backward(const void *d_normed, const void *d_residual, const void *residual,
+                                 const float *rstd, const void *y, int M, int C, const void *post_weight,
+                                 const void *gate, int gate_kind, float residual_scale, const void *pre_weight,
+                                 float weight_offset, void *d_x, void *d_y, void *d_pre_weight,
+                                 void *d_post_weight, void *d_gate, void *workspace, size_t workspace_bytes,
+                                 void *stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *w4_status_string(int status);
