@@ -21,6 +21,7 @@
 #include "quantize.cuh"
 #include "w4a16.h"
 #include "w8_gemm.cuh"
+#include "w8_gemm_tc.cuh"
 #include "w8_quantize.cuh"
 
 namespace {

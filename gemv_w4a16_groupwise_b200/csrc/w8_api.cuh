@@ -20,13 +20,80 @@ w4_status run_quantize_rows(const uint16_t* X, int R, int C, const float* channe
     return launch_status();
 }
 
-w4_status run_w8_gemm(const w4::W8Args& a, bool transposed, cudaStream_t st) {
-    const int out = transposed ? a.K : a.N;
-    const dim3 grid((out + 63) / 64, (a.M + 63) / 64);
-    if (grid.y > 65535) return W4_ERR_UNSUPPORTED;
-    if (transposed) launch_pdl(w4::w8_gemm_simple_kernel<true>, grid, dim3(256), 0, st, a);
-    else launch_pdl(w4::w8_gemm_simple_kernel<false>, grid, dim3(256), 0, st, a);
+// The tensor-core product's plan: the token tile, whole tiles F and the pairs
+// that share the others' reduction.
+struct W8Plan {
+    int TN = 32, tiles_m = 1, tiles = 1, F = 0, chunks = 1, cut_pairs = 1, grid_pairs = 1;
+    size_t ws = 0;
+};
+
+W8Plan plan_w8(int M, int N, int K, bool transposed, int sms) {
+    W8Plan p;
+    const int out = transposed ? K : N, red = transposed ? N : K;
+    p.TN = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    p.tiles_m = (M + p.TN - 1) / p.TN;
+    p.tiles = p.tiles_m * ((out + w4::kW8Rows - 1) / w4::kW8Rows);
+    p.chunks = (red + w4::kW8Red - 1) / w4::kW8Red;
+    const int pairs = std::max(1, sms / 2);
+    const int rem = p.tiles % pairs;
+    // a last wave that is nearly full runs as whole tiles; an emptier one is
+    // cut over all pairs, at least 4 stages each
+    p.F = rem * 4 > pairs * 3 ? p.tiles : p.tiles - rem;
+    const long long total = static_cast<long long>(p.tiles - p.F) * p.chunks;
+    p.cut_pairs = static_cast<int>(std::max<long long>(1, std::min<long long>(pairs, total / 4)));
+    p.grid_pairs = std::max(std::min(p.F, pairs), total > 0 ? p.cut_pairs : 1);
+    // one pair per tile leaves nothing to add up
+    p.ws = p.cut_pairs > 1 && total > 0
+               ? static_cast<size_t>(2) * p.cut_pairs * p.TN * w4::kW8Rows * sizeof(int32_t) : 0;
+    return p;
+}
+
+// int8 rows, `ld` bytes apart, in boxes of 128 bytes x box_rows with the
+// 128-byte swizzle; out-of-range bytes read as 0.
+bool make_map_i8(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[2] = {cols, rows};
+    cuuint64_t gstride[1] = {ld};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), gdim, gstride, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool TR, int TN>
+w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, const DeviceInfo& di, cudaStream_t st) {
+    constexpr int kStage = w4::w8_stage_bytes(TN);
+    const size_t fixed = 1024 + w4::kW8EpiBytes + 128;
+    const int stages = std::min(10, static_cast<int>((di.max_smem_optin - fixed) / (kStage + 16)));
+    if (di.max_smem_optin < 200 * 1024 || stages < 2) return W4_ERR_UNSUPPORTED;
+    const size_t smem = fixed + static_cast<size_t>(stages) * (kStage + 16);
+    CUtensorMap wmap, amap;
+    const int red = TR ? g.N : g.K;
+    if (!make_map_i8(&wmap, g.W, g.N, g.K, g.ldw, 128) || !make_map_i8(&amap, g.A, g.M, red, g.lda, TN / 2))
+        return W4_ERR_CUDA;
+    auto fn = w4::w8_gemm_tc_kernel<TR, TN>;
+    if (ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
+    const w4::W8TcArgs a = {g, part, p.tiles_m, p.tiles, p.F, p.chunks, p.cut_pairs, stages};
+    launch_pdl(fn, dim3(2 * p.grid_pairs), dim3(w4::kW8Threads), smem, st, wmap, amap, a);
+    const w4_status s = launch_status();
+    if (s != W4_OK || p.ws == 0) return s;
+    const long long threads = static_cast<long long>(p.tiles - p.F) * TN * (w4::kW8Rows / 4);
+    launch_pdl(w4::w8_finalize_kernel<TR>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, st, a, TN);
     return launch_status();
+}
+
+w4_status run_w8_gemm(const w4::W8Args& a, bool transposed, void* ws, cudaStream_t st) {
+    const DeviceInfo di = device_info(current_device());
+    const W8Plan p = plan_w8(a.M, a.N, a.K, transposed, di.sms);
+    int32_t* part = static_cast<int32_t*>(ws);
+    switch (p.TN) {
+        case 32: return transposed ? launch_w8_tc<true, 32>(p, a, part, di, st) : launch_w8_tc<false, 32>(p, a, part, di, st);
+        case 64: return transposed ? launch_w8_tc<true, 64>(p, a, part, di, st) : launch_w8_tc<false, 64>(p, a, part, di, st);
+        case 128: return transposed ? launch_w8_tc<true, 128>(p, a, part, di, st) : launch_w8_tc<false, 128>(p, a, part, di, st);
+        default: return transposed ? launch_w8_tc<true, 256>(p, a, part, di, st) : launch_w8_tc<false, 256>(p, a, part, di, st);
+    }
 }
 
 }  // namespace
@@ -43,18 +110,15 @@ w4_status w8_quantize_rows(const void* X, int R, int C, const float* channel_sca
 }
 
 size_t w8a8_workspace_bytes(int M, int N, int K, int transposed) {
-    (void)M;
-    (void)N;
-    (void)K;
-    (void)transposed;
-    return 0;
+    if (M <= 0 || N <= 0 || K <= 0) return 0;
+    return plan_w8(M, N, K, transposed != 0, device_info(current_device()).sms).ws;
 }
 
 // the tokens' codes and scales lie in front of the product's own workspace
 size_t w8a8_linear_workspace_bytes(int M, int N, int K, int transposed) {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
     const size_t red = round16(static_cast<size_t>(transposed ? N : K));
-    return M * red + round16(M * sizeof(float)) + w8a8_workspace_bytes(M, N, K, transposed);
+    return round16(M * red) + round16(M * sizeof(float)) + w8a8_workspace_bytes(M, N, K, transposed);
 }
 
 w4_status w8a8_gemm(const int8_t* A, long long lda, const float* a_scales, int M, int N, int K, const int8_t* W,
@@ -71,7 +135,7 @@ w4_status w8a8_gemm(const int8_t* A, long long lda, const float* a_scales, int M
     if (!aligned16(workspace)) return W4_ERR_ALIGNMENT;
     const w4::W8Args a = {A, a_scales, W, w_scales, static_cast<const uint16_t*>(bias),
                           static_cast<uint16_t*>(Y), lda, ldw, M, N, K};
-    return run_w8_gemm(a, transposed != 0, static_cast<cudaStream_t>(stream));
+    return run_w8_gemm(a, transposed != 0, workspace, static_cast<cudaStream_t>(stream));
 }
 
 w4_status w8a8_linear(const void* A, int M, int N, int K, const int8_t* W, long long ldw, const float* w_scales,
@@ -93,7 +157,7 @@ w4_status w8a8_linear(const void* A, int M, int N, int K, const int8_t* W, long 
     if (q != W4_OK) return q;
     const w4::W8Args a = {codes, scales, W, transposed ? nullptr : w_scales, static_cast<const uint16_t*>(bias),
                           static_cast<uint16_t*>(Y), static_cast<long long>(ld), ldw, M, N, K};
-    return run_w8_gemm(a, transposed != 0, st);
+    return run_w8_gemm(a, transposed != 0, reinterpret_cast<uint8_t*>(scales) + round16(M * sizeof(float)), st);
 }
 
 }  // extern "C"

@@ -1,0 +1,415 @@
+// 8-bit product on the tensor cores: TMA -> tcgen05.mma kind::i8 by CTA pairs
+// -> int32 in tensor memory -> scales, bias, bf16.
+//
+//     forward     D[n, m] = sum_k w[n, k] a[m, k]      weights K-major
+//     transposed  D[k, m] = sum_n w[n, k] a[m, n]      weights MN-major, as they lie
+//
+// The weights take the MMA's 256-row side (128 rows in each CTA of the pair)
+// and the tokens its column side, TN in {32, 64, 128, 256}: one kernel serves
+// a few dozen tokens and thousands.  A stage holds 128 of the reduction: the
+// CTA's 16 KB of weights and its half of the token tile (TN / 2 rows); with
+// pairs an SM fetches 32 KB for 256 x 256 x 128 / 2 products instead of the 48
+// of a 128 x 256 tile of its own, and it is the fetch from L2 that a wider
+// tile on one SM would wait for.
+//
+// Persistent: pair p takes whole tiles p, p + P, ... below F, then a share of
+// the remaining tiles' reduction slices, cut evenly over the pairs across tile
+// borders.  A tile cut that way leaves int32 partials (exact, so their order
+// does not matter) which w8_finalize_kernel adds, scales and rounds.
+//
+// Warps: 0 TMA producer, 1 MMA issuer (in the pair's first CTA), 2..5
+// epilogue.  Accumulators are double buffered, so a tile's epilogue runs
+// beside the next tile's products.  Full barriers live in the first CTA and
+// count both CTAs' bytes; the stage's release and the accumulator's
+// completion are committed to both.
+#pragma once
+
+#include "gemm_tc.cuh"
+#include "tma.cuh"
+#include "w8_gemm.cuh"
+
+namespace w4 {
+
+constexpr int kW8Rows = 256;          // outputs of a pair's tile
+constexpr int kW8Red = 128;           // reduction of a stage
+constexpr int kW8ABytes = 128 * kW8Red;
+constexpr int kW8EpiWarps = 4;
+constexpr int kW8Threads = 64 + 32 * kW8EpiWarps;
+constexpr int kW8StageTokens = 32;    // tokens an epilogue warp stages at a time
+constexpr int kW8EpiBytes = kW8EpiWarps * kW8StageTokens * 32 * 2;
+
+__host__ __device__ constexpr int w8_stage_bytes(int TN) { return kW8ABytes + TN / 2 * kW8Red; }
+
+struct W8TcArgs {
+    W8Args p;
+    int32_t* part;       // [2 pairs][TN][256] partial tiles
+    int tiles_m, tiles;  // token tiles, tiles in all
+    int F;               // tiles below F are whole units
+    int chunks;          // stages of one tile
+    int cut_pairs;       // pairs that share the tiles from F on
+    int stages;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t first_cta_addr(const void* p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 2-D load into this CTA's shared memory that completes on the pair's first CTA's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void umma_i8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once the MMAs before are done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Instruction descriptor: s8 x s8 -> s32, M = 256 over the pair, N = TN.
+__host__ __device__ constexpr uint32_t umma_idesc_i8(int TN, bool a_mn_major) {
+    return (2u << 4)                              // D format s32
+           | (1u << 7)                            // A format s8
+           | (1u << 10)                           // B format s8
+           | ((a_mn_major ? 1u : 0u) << 15)       // A major
+           | (static_cast<uint32_t>(TN >> 3) << 17)
+           | (static_cast<uint32_t>(kW8Rows >> 4) << 24);
+}
+
+// The units of pair p of P, in order.
+struct W8Unit {
+    int tile, kb0, kb1;
+    int part;            // slot of the partial tile, or -1 for a whole tile
+};
+struct W8Walk {
+    int p, P, F, chunks;
+    int next_whole;
+    long long c, c1;     // the pair's share of the cut tiles' stages
+    int cut_units;
+    __device__ W8Walk(const W8TcArgs& a, int pair, int pairs) {
+        p = pair;
+        P = pairs;
+        F = a.F;
+        chunks = a.chunks;
+        next_whole = pair;
+        const long long total = pair < a.cut_pairs ? static_cast<long long>(a.tiles - a.F) * a.chunks : 0;
+        c = total * pair / a.cut_pairs;
+        c1 = total * (pair + 1) / a.cut_pairs;
+        cut_units = 0;
+    }
+    __device__ bool next(W8Unit* u) {
+        if (next_whole < F) {
+            *u = W8Unit{next_whole, 0, chunks, -1};
+            next_whole += P;
+            return true;
+        }
+        if (c >= c1) return false;
+        const int t = static_cast<int>(c / chunks);
+        u->tile = F + t;
+        u->kb0 = static_cast<int>(c - static_cast<long long>(t) * chunks);
+        u->kb1 = static_cast<int>(min(static_cast<long long>(chunks), u->kb0 + (c1 - c)));
+        u->part = (u->kb0 == 0 && u->kb1 == chunks) ? -1 : 2 * p + (cut_units > 0 ? 1 : 0);
+        ++cut_units;
+        c += u->kb1 - u->kb0;
+        return true;
+    }
+};
+
+template <bool TR, int TN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
+    w8_gemm_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
+                      const W8TcArgs a) {
+    static_assert(TN == 32 || TN == 64 || TN == 128 || TN == 256, "TN");
+    constexpr int kStageBytes = w8_stage_bytes(TN);
+    constexpr uint32_t kTmemCols = 2 * TN;
+    constexpr uint32_t kIdesc = umma_idesc_i8(TN, TR);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int NS = a.stages;
+    uint8_t* epi = base + NS * kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(epi + kW8EpiBytes);
+    uint64_t* empty = full + NS;
+    uint64_t* acc_full = empty + NS;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int out = TR ? a.p.K : a.p.N;
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&wmap);
+        tma_prefetch_desc(&amap);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 2 * kW8EpiWarps);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();        // both CTAs' barriers stand before either uses them
+    tc_fence_after();
+    const uint32_t tmem_d = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    W8Walk walk(a, pair, pairs);
+    W8Unit u;
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int s = 0;
+            uint32_t round = 0;
+            bool ok = true;
+            while (ok && walk.next(&u)) {
+                const int m0 = (u.tile % a.tiles_m) * TN + static_cast<int>(rank) * (TN / 2);
+                const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
+                for (int kb = u.kb0; kb < u.kb1; ++kb) {
+                    if (round > 0 && !mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = base + s * kStageBytes;
+                    const uint32_t bar = first_cta_addr(&full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                    if (TR) tma_load_2d_pair(st, &wmap, o0, kb * kW8Red, bar);
+                    else tma_load_2d_pair(st, &wmap, kb * kW8Red, o0, bar);
+                    tma_load_2d_pair(st + kW8ABytes, &amap, kb * kW8Red, m0, bar);
+                    if (++s == NS) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            // the releases of the stages still in use come from the other CTA:
+            // see them in before this one may leave
+            for (int j = 0; j < NS && ok; ++j) {
+                if (round > 0) ok = mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty);
+                if (++s == NS) {
+                    s = 0;
+                    ++round;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0 && rank == 0) {
+            bool ok = true;
+            int s = 0, i = 0;
+            uint32_t phase = 0;
+            while (ok && walk.next(&u)) {
+                const int buf = i & 1;
+                if (i >= 2) ok = mbar_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1u, abort_flag, kErrTimeoutAccum);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem_d + static_cast<uint32_t>(buf) * TN;
+                for (int kb = u.kb0; kb < u.kb1; ++kb) {
+                    ok = mbar_wait_bounded(&full[s], phase, abort_flag, kErrTimeoutTmaFull);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(base + s * kStageBytes);
+                    const uint32_t b_addr = a_addr + kW8ABytes;
+#pragma unroll
+                    for (int j = 0; j < kW8Red / 32; ++j) {
+                        // MN-major: 32 reduction rows are four groups of 8 rows, 1024 bytes each
+                        const uint64_t adesc = TR ? umma_desc_sw128(a_addr + j * 4096, kW8ABytes, 1024)
+                                                  : umma_desc_sw128(a_addr + j * 32, 16, 1024);
+                        const uint64_t bdesc = umma_desc_sw128(b_addr + j * 32, 16, 1024);
+                        umma_i8_pair(acc, adesc, bdesc, kIdesc, (kb != u.kb0 || j != 0) ? 1u : 0u);
+                    }
+                    umma_commit_pair(&empty[s]);
+                    if (++s == NS) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                umma_commit_pair(&acc_full[buf]);   // also tracks any MMA issued before an abort
+                ++i;
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue
+        const int q = warp & 3;                 // TMEM lanes 32 q .. 32 q + 31
+        uint16_t* stage = reinterpret_cast<uint16_t*>(epi) + (warp - 2) * kW8StageTokens * 32;
+        int i = 0;
+        while (walk.next(&u)) {
+            const int buf = i & 1;
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, abort_flag,
+                                                                      kErrTimeoutAccum));
+            if (!ok || *abort_flag) break;
+            tc_fence_after();
+            const int m0 = (u.tile % a.tiles_m) * TN;
+            const int row = static_cast<int>(rank) * 128 + 32 * q + lane;      // in the tile
+            const int o0 = (u.tile / a.tiles_m) * kW8Rows;
+            const int o = o0 + row;
+            const bool ov = o < out;
+            const uint32_t acc = tmem_d + static_cast<uint32_t>(buf) * TN + (static_cast<uint32_t>(32 * q) << 16);
+            const float ws = (!TR && ov) ? a.p.w_scales[o] : 1.0f;
+            const float bias = (a.p.bias && ov) ? bf16_bits_to_float(a.p.bias[o]) : 0.0f;
+            const int tokens = min(TN, a.p.M - m0);
+#pragma unroll 1
+            for (int c0 = 0; c0 < tokens; c0 += 32) {
+                uint32_t r[32];
+                tmem_ld_x32(acc + static_cast<uint32_t>(c0), r);
+                if (u.part >= 0) {
+                    int32_t* pt = a.part + (static_cast<size_t>(u.part) * TN + c0) * kW8Rows + row;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) pt[e * kW8Rows] = static_cast<int32_t>(r[e]);
+                    continue;
+                }
+                const float as = (m0 + c0 + lane < a.p.M) ? a.p.a_scales[m0 + c0 + lane] : 0.0f;
+                if ((out & 7) == 0) {
+                    // through shared memory: [token][32 outputs], then 16 bytes a lane
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        stage[e * 32 + lane] = w8_output(static_cast<int>(r[e]),
+                                                         __shfl_sync(0xFFFFFFFFu, as, e) * ws, bias);
+                    __syncwarp();
+                    const int ol = o0 + static_cast<int>(rank) * 128 + 32 * q + (lane & 3) * 8;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int t = g * 8 + (lane >> 2);
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + t * 32 + (lane & 3) * 8);
+                        if (m0 + c0 + t < a.p.M && ol < out)
+                            *reinterpret_cast<uint4*>(a.p.Y + static_cast<size_t>(m0 + c0 + t) * out + ol) = v;
+                    }
+                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const uint16_t y = w8_output(static_cast<int>(r[e]), __shfl_sync(0xFFFFFFFFu, as, e) * ws, bias);
+                        if (m0 + c0 + e < a.p.M && ov) a.p.Y[static_cast<size_t>(m0 + c0 + e) * out + o] = y;
+                    }
+                }
+            }
+            // this warp's reads of the buffer are complete
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(first_cta_addr(&acc_empty[buf]));
+            ++i;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        // a role gave up: let copies and mma already issued land (bounded)
+        // before the tensor memory and the CTAs' shared memory are released
+        const unsigned long long t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+    }
+    cluster_sync();        // neither CTA leaves while the other may still reach into it
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_d), "r"(kTmemCols) : "memory");
+    }
+}
+
+// The cut tiles: Y = bf16(sum of the partials * scales + bias).  One thread
+// per token and four outputs; a tile that one pair computed whole is already
+// stored.  The pair whose share [total p / P, total (p + 1) / P) holds stage c
+// is ((c + 1) P - 1) / total.
+template <bool TR>
+__global__ void __launch_bounds__(256) w8_finalize_kernel(const W8TcArgs a, int TN) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int pairs = a.cut_pairs;
+    const int out = TR ? a.p.K : a.p.N;
+    const int per_tile = TN * (kW8Rows / 4);
+    const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const int tt = static_cast<int>(idx / per_tile);
+    if (tt >= a.tiles - a.F) return;
+    const int e = static_cast<int>(idx - static_cast<long long>(tt) * per_tile);
+    const int tok = e / (kW8Rows / 4), rl = (e % (kW8Rows / 4)) * 4;
+    const int t = a.F + tt;
+    const int m = (t % a.tiles_m) * TN + tok, o = (t / a.tiles_m) * kW8Rows + rl;
+    if (m >= a.p.M || o >= out) return;
+    const long long total = static_cast<long long>(a.tiles - a.F) * a.chunks;
+    const long long first = static_cast<long long>(tt) * a.chunks;
+    const int p0 = static_cast<int>(((first + 1) * pairs - 1) / total);
+    const int p1 = static_cast<int>(((first + a.chunks) * pairs - 1) / total);
+    if (p0 == p1) return;
+    int4 s = make_int4(0, 0, 0, 0);
+    for (int p = p0; p <= p1; ++p) {
+        // the pair's first unit lies in this tile, or in an earlier one
+        const bool first_unit = total * p / pairs >= first;
+        const int slot = 2 * p + (first_unit ? 0 : 1);
+        const int4 v = *reinterpret_cast<const int4*>(a.part + (static_cast<size_t>(slot) * TN + tok) * kW8Rows + rl);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    const int v[4] = {s.x, s.y, s.z, s.w};
+    const float as = a.p.a_scales[m];
+    uint16_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool ok = o + i < out;
+        const float ws = (!TR && ok) ? a.p.w_scales[o + i] : 1.0f;
+        y[i] = w8_output(v[i], as * ws, (a.p.bias && ok) ? bf16_bits_to_float(a.p.bias[o + i]) : 0.0f);
+    }
+    uint16_t* dst = a.p.Y + static_cast<size_t>(m) * out + o;
+    if ((out & 3) == 0) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(y[0] | (static_cast<uint32_t>(y[1]) << 16),
+                                                    y[2] | (static_cast<uint32_t>(y[3]) << 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (o + i < out) dst[i] = y[i];
+    }
+}
+
+}  // namespace w4
