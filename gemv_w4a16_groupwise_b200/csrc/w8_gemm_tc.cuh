@@ -60,8 +60,10 @@ __device__ __forceinline__ uint32_t first_cta_addr(const void* p) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
     return r;
 }
+// The form without .aligned counts threads, so it holds for a warp whose lanes
+// arrive apart.
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 // 2-D load into this CTA's shared memory that completes on the pair's first CTA's barrier.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
@@ -190,6 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         *abort_flag = 0;
         fence_barrier_init();
     }
+    __syncwarp();
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
@@ -287,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
             const int buf = i & 1;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, abort_flag,
                                                                       kErrTimeoutAccum));
-            if (!ok || *abort_flag) break;
+            if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) break;
             tc_fence_after();
             const int m0 = (u.tile % a.tiles_m) * TN;
             const int row = static_cast<int>(rank) * 128 + 32 * q + lane;      // in the tile
@@ -301,6 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
 #pragma unroll 1
             for (int c0 = 0; c0 < tokens; c0 += 32) {
                 uint32_t r[32];
+                __syncwarp();
                 tmem_ld_x32(acc + static_cast<uint32_t>(c0), r);
                 if (u.part >= 0) {
                     int32_t* pt = a.part + (static_cast<size_t>(u.part) * TN + c0) * kW8Rows + row;
@@ -341,6 +345,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         }
     }
 
+    // The lanes of a warp whose lane 0 alone had a role come together here:
+    // the collective instructions below take whole warps, and a deallocation
+    // that each part of a split warp issued would free the tensor memory of
+    // whatever runs on the SM next.
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) {
@@ -351,6 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         }
     }
     cluster_sync();        // neither CTA leaves while the other may still reach into it
+    __syncwarp();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_d), "r"(kTmemCols) : "memory");
