@@ -4,18 +4,6 @@
 
 namespace {
 
-// The block of a row of C: the fewest threads that hold it in one vector of
-// 8 each, up to 512, then two vectors each.
-template <template <int, int, int> class Launch, typename... Args>
-w4_status dispatch_row(int C, Args... args) {
-    const bool vec = C % 8 == 0;
-    if (C <= 1024) return vec ? Launch<128, 1, 8>::run(args...) : Launch<128, 8, 1>::run(args...);
-    if (C <= 2048) return vec ? Launch<256, 1, 8>::run(args...) : Launch<256, 8, 1>::run(args...);
-    if (C <= 4096) return vec ? Launch<256, 2, 8>::run(args...) : Launch<256, 16, 1>::run(args...);
-    if (C <= 8192) return vec ? Launch<512, 2, 8>::run(args...) : Launch<512, 16, 1>::run(args...);
-    return vec ? Launch<1024, 2, 8>::run(args...) : Launch<1024, 16, 1>::run(args...);
-}
-
 template <int T, int V, int VEC>
 struct NormLaunch {
     static w4_status run(const w4::NormArgs& a, cudaStream_t st) {
@@ -54,7 +42,7 @@ w4_status w4_block_norm(const void* x, const void* y, int M, int C, const void* 
                         int gate_kind, float residual_scale, const void* pre_weight, float weight_offset, float eps,
                         void* residual, void* normed, long long ld, float* scales, float* rstd, void* stream) {
     if (M <= 0 || C <= 0) return W4_ERR_INVALID_ARG;
-    if (C > w4::kNormMaxC) return W4_ERR_UNSUPPORTED;
+    if (C > w4::kRowMaxC) return W4_ERR_UNSUPPORTED;
     if (!gate_ok(gate_kind, gate, y) || !(eps > 0.0f) || !(eps < 3.4e38f)) return W4_ERR_INVALID_ARG;
     if (!x || !pre_weight || !normed || (post_weight && !y) || (residual != nullptr) != (y != nullptr))
         return W4_ERR_INVALID_ARG;
@@ -96,7 +84,7 @@ w4_status w4_block_norm_backward(const void* d_normed, const void* d_residual, c
                                  float weight_offset, void* d_x, void* d_y, void* d_pre_weight, void* d_post_weight,
                                  void* d_gate, void* workspace, size_t workspace_bytes, void* stream) {
     if (M <= 0 || C <= 0) return W4_ERR_INVALID_ARG;
-    if (C > w4::kNormMaxC) return W4_ERR_UNSUPPORTED;
+    if (C > w4::kRowMaxC) return W4_ERR_UNSUPPORTED;
     if (!gate_ok(gate_kind, gate, y)) return W4_ERR_INVALID_ARG;
     if (!d_normed || !residual || !rstd || !pre_weight || !d_x || !d_pre_weight || (post_weight && !y))
         return W4_ERR_INVALID_ARG;

@@ -22,6 +22,7 @@
 #include "w4a16.h"
 #include "w8_gemm.cuh"
 #include "w8_gemm_tc.cuh"
+#include "w8_gemv.cuh"
 #include "w8_quantize.cuh"
 
 namespace {

@@ -14,9 +14,42 @@ w4_status check_w8(int M, int N, int K, long long ldw, int transposed, const voi
     return W4_OK;
 }
 
+// The block of a row of C: the fewest threads that hold it in one vector of
+// 8 each, up to 512, then two vectors each.
+template <template <int, int, int> class Launch, typename... Args>
+w4_status dispatch_row(int C, Args... args) {
+    const bool vec = C % 8 == 0;
+    if (C <= 1024) return vec ? Launch<128, 1, 8>::run(args...) : Launch<128, 8, 1>::run(args...);
+    if (C <= 2048) return vec ? Launch<256, 1, 8>::run(args...) : Launch<256, 8, 1>::run(args...);
+    if (C <= 4096) return vec ? Launch<256, 2, 8>::run(args...) : Launch<256, 16, 1>::run(args...);
+    if (C <= 8192) return vec ? Launch<512, 2, 8>::run(args...) : Launch<512, 16, 1>::run(args...);
+    return vec ? Launch<1024, 2, 8>::run(args...) : Launch<1024, 16, 1>::run(args...);
+}
+
+template <int T, int V, int VEC>
+struct QuantizeLaunch {
+    static w4_status run(const uint16_t* X, int R, int C, const float* channel, int8_t* codes, long long ld,
+                         float* scales, int sms, cudaStream_t st) {
+        const int grid = std::min(R, sms * (2048 / T));     // what the SMs hold at once
+        if (channel)
+            launch_pdl(w4::quantize_rows_kernel<T, V, VEC, true>, dim3(grid), dim3(T), 0, st, X, R, C, channel, codes,
+                       ld, scales);
+        else
+            launch_pdl(w4::quantize_rows_kernel<T, V, VEC, false>, dim3(grid), dim3(T), 0, st, X, R, C, channel, codes,
+                       ld, scales);
+        return launch_status();
+    }
+};
+
 w4_status run_quantize_rows(const uint16_t* X, int R, int C, const float* channel, int8_t* codes, long long ld,
                             float* scales, cudaStream_t st) {
-    launch_pdl(w4::quantize_rows_kernel, dim3(R), dim3(512), 0, st, X, C, channel, codes, ld, scales);
+    if (C <= w4::kRowMaxC)
+        return dispatch_row<QuantizeLaunch>(C, X, R, C, channel, codes, ld, scales,
+                                            device_info(current_device()).sms, st);
+    if (C % 8 == 0)
+        launch_pdl(w4::quantize_long_rows_kernel<8>, dim3(R), dim3(1024), 0, st, X, C, channel, codes, ld, scales);
+    else
+        launch_pdl(w4::quantize_long_rows_kernel<1>, dim3(R), dim3(1024), 0, st, X, C, channel, codes, ld, scales);
     return launch_status();
 }
 
@@ -84,7 +117,33 @@ w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, cons
     return launch_status();
 }
 
+// The stream kernel serves forward products of a few tokens.
+bool w8_gemv_serves(int M, bool transposed) { return !transposed && M <= w4::kGvMaxTokens; }
+
+// Whether w8_gemv_kernel quantizes the tokens itself, and for how many at
+// once (1, 2 or 4; 0: it does not): rows of whole 16 bytes, at most
+// kGvFusedValues values.
+int w8_gemv_fused(int M, int K, bool transposed) {
+    if (transposed || M > 4 || K % 8 != 0) return 0;
+    const int MT = M > 2 ? 4 : M;
+    return static_cast<long long>(MT) * K <= w4::kGvFusedValues ? MT : 0;
+}
+
+template <int MT>
+w4_status launch_w8_gemv(const w4::W8Args& p, const uint16_t* X, cudaStream_t st) {
+    const w4::W8GemvArgs a = {p, X};
+    const size_t smem =
+        MT > 0 ? static_cast<size_t>(MT) * w4::w8_gemv_token_bytes(p.K) + 2 * w4::kGvFusedValues : 0;
+    if (smem > 40 * 1024 &&
+        ensure_smem(reinterpret_cast<const void*>(w4::w8_gemv_kernel<MT>), smem) != cudaSuccess)
+        return W4_ERR_CUDA;
+    launch_pdl(w4::w8_gemv_kernel<MT>, dim3((p.N + w4::kGvRows - 1) / w4::kGvRows), dim3(w4::kGvWarps * 32),
+               smem, st, a);
+    return launch_status();
+}
+
 w4_status run_w8_gemm(const w4::W8Args& a, bool transposed, void* ws, cudaStream_t st) {
+    if (w8_gemv_serves(a.M, transposed)) return launch_w8_gemv<0>(a, nullptr, st);
     const DeviceInfo di = device_info(current_device());
     const W8Plan p = plan_w8(a.M, a.N, a.K, transposed, di.sms);
     int32_t* part = static_cast<int32_t*>(ws);
@@ -110,13 +169,13 @@ w4_status w8_quantize_rows(const void* X, int R, int C, const float* channel_sca
 }
 
 size_t w8a8_workspace_bytes(int M, int N, int K, int transposed) {
-    if (M <= 0 || N <= 0 || K <= 0) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || w8_gemv_serves(M, transposed != 0)) return 0;
     return plan_w8(M, N, K, transposed != 0, device_info(current_device()).sms).ws;
 }
 
 // the tokens' codes and scales lie in front of the product's own workspace
 size_t w8a8_linear_workspace_bytes(int M, int N, int K, int transposed) {
-    if (M <= 0 || N <= 0 || K <= 0) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || w8_gemv_fused(M, K, transposed != 0)) return 0;
     const size_t red = round16(static_cast<size_t>(transposed ? N : K));
     return round16(M * red) + round16(M * sizeof(float)) + w8a8_workspace_bytes(M, N, K, transposed);
 }
@@ -145,9 +204,16 @@ w4_status w8a8_linear(const void* A, int M, int N, int K, const int8_t* W, long 
     if (s != W4_OK && s != W4_ERR_ALIGNMENT) return s;
     if (!A || !w_scales) return W4_ERR_INVALID_ARG;
     if (s != W4_OK || !aligned16(A) || !aligned16(w_scales)) return W4_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < w8a8_linear_workspace_bytes(M, N, K, transposed)) return W4_ERR_WORKSPACE;
+    const size_t need = w8a8_linear_workspace_bytes(M, N, K, transposed);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return W4_ERR_WORKSPACE;
     if (!aligned16(workspace)) return W4_ERR_ALIGNMENT;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (const int MT = w8_gemv_fused(M, K, transposed != 0)) {
+        const w4::W8Args p = {nullptr, nullptr, W, w_scales, static_cast<const uint16_t*>(bias),
+                              static_cast<uint16_t*>(Y), 0, ldw, M, N, K};
+        const uint16_t* X = static_cast<const uint16_t*>(A);
+        return MT == 1 ? launch_w8_gemv<1>(p, X, st) : MT == 2 ? launch_w8_gemv<2>(p, X, st) : launch_w8_gemv<4>(p, X, st);
+    }
     const int red = transposed ? N : K;
     const size_t ld = round16(red);
     int8_t* codes = static_cast<int8_t*>(workspace);

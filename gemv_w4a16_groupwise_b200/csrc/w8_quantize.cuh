@@ -16,7 +16,7 @@
 // that inv, rounded up, leans to.
 #pragma once
 
-#include "common.cuh"
+#include "rows.cuh"
 
 namespace w4 {
 
@@ -61,43 +61,115 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const RowScale& s) 
     return make_uint2(codes4(v[0], v[1], v[2], v[3], s), codes4(v[4], v[5], v[6], v[7], s));
 }
 
-// Maximum of the bit patterns over the block (order-independent; as bits, a
-// NaN is larger than an infinity and neither is dropped).
-template <int T>
-__device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* buf) {
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if constexpr (T == 32) return v;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    uint32_t t = 0;
+// The channel factors of a thread's columns, kept over its rows.
+template <int T, int V, int VEC>
+struct ChannelSpan {
+    using S = RowSpan<T, V, VEC>;
+    float f[S::E];
+    __device__ __forceinline__ void load(const float* channel, int C) {
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) t = max(t, buf[w]);
-    return t;
+        for (int j = 0; j < V; ++j) {
+            const int c = S::col(j);
+            if constexpr (VEC == 8) {
+                const bool in = c < C;
+                const float4 lo = in ? *reinterpret_cast<const float4*>(channel + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 hi = in ? *reinterpret_cast<const float4*>(channel + c + 4) : lo;
+                f[8 * j] = lo.x, f[8 * j + 1] = lo.y, f[8 * j + 2] = lo.z, f[8 * j + 3] = lo.w;
+                f[8 * j + 4] = hi.x, f[8 * j + 5] = hi.y, f[8 * j + 6] = hi.z, f[8 * j + 7] = hi.w;
+            } else {
+                f[j] = c < C ? channel[c] : 0.0f;
+            }
+        }
+    }
+};
+
+// Rows of at most 16384: a block holds a row in registers between the maximum
+// and the codes, so the row is read once.  Bound by device memory (3 bytes an
+// element).  Blocks walk over the rows and keep the channel factors, which
+// would otherwise be twice a row's own bytes from L2 every time.
+template <int T, int V, int VEC, bool CHANNEL>
+__global__ void __launch_bounds__(T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
+                                                          const float* __restrict__ channel,
+                                                          int8_t* __restrict__ codes, long long ld,
+                                                          float* __restrict__ scales) {
+    using S = RowSpan<T, V, VEC>;
+    __shared__ uint32_t buf[2][32];
+    pdl_wait();
+    pdl_launch_dependents();
+    ChannelSpan<T, V, VEC> ch;
+    if constexpr (CHANNEL) ch.load(channel, C);
+    int turn = 0;
+    for (long long m = blockIdx.x; m < R; m += gridDim.x, turn ^= 1) {
+        uint32_t p[S::W];
+        S::load(p, X + static_cast<size_t>(m) * C, C);
+        auto value = [&](int e) { return CHANNEL ? S::get(p, e) * ch.f[e] : S::get(p, e); };
+        uint32_t top = 0;       // columns past C read as 0
+#pragma unroll
+        for (int e = 0; e < S::E; ++e) top = max(top, abs_bits(value(e)));
+        top = block_max_bits<T>(top, buf[turn]);
+        const RowScale sc = row_scale(__uint_as_float(top));
+        if (threadIdx.x == 0) scales[m] = sc.scale;
+        int8_t* q = codes + static_cast<size_t>(m) * ld;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = S::col(j);
+            if (c < C) {
+                if constexpr (VEC == 8) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = value(8 * j + i);
+                    *reinterpret_cast<uint2*>(q + c) = codes8(v, sc);
+                } else {
+                    q[c] = code1(value(j), sc);
+                }
+            }
+        }
+    }
 }
 
-// One block per row: the largest magnitude, then the codes from a second read
-// of the row (an L1 or L2 hit).  channel (fp32 [C], or null) multiplies the
-// values first, rounded to fp32.
-__global__ void __launch_bounds__(512) quantize_rows_kernel(const uint16_t* __restrict__ X, int C,
-                                                            const float* __restrict__ channel,
-                                                            int8_t* __restrict__ codes, long long ld,
-                                                            float* __restrict__ scales) {
+// Longer rows: the second pass reads the row again (from L2).
+template <int VEC>
+__global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t* __restrict__ X, int C,
+                                                                  const float* __restrict__ channel,
+                                                                  int8_t* __restrict__ codes, long long ld,
+                                                                  float* __restrict__ scales) {
     __shared__ uint32_t buf[32];
-    const long long m = blockIdx.x;
-    const uint16_t* x = X + static_cast<size_t>(m) * C;
-    pdl_launch_dependents();
+    const size_t m = blockIdx.x;
+    const uint16_t* x = X + m * C;
     pdl_wait();
-    auto value = [&](int c) {
-        const float v = bf16_bits_to_float(x[c]);
-        return channel ? v * channel[c] : v;
+    pdl_launch_dependents();
+    auto load = [&](int c, float (&v)[VEC]) {
+        if constexpr (VEC == 8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(x + c);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((i & 1) ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+        } else {
+            v[0] = bf16_bits_to_float(x[c]);
+        }
+        if (channel) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] *= channel[c + i];
+        }
     };
     uint32_t top = 0;
-    for (int c = threadIdx.x; c < C; c += 512) top = max(top, abs_bits(value(c)));
-    top = block_max_bits<512>(top, buf);
-    const RowScale sc = row_scale(__uint_as_float(top));
+#pragma unroll 2
+    for (int c = threadIdx.x * VEC; c < C; c += 1024 * VEC) {
+        float v[VEC];
+        load(c, v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) top = max(top, abs_bits(v[i]));
+    }
+    const RowScale sc = row_scale(__uint_as_float(block_max_bits<1024>(top, buf)));
     if (threadIdx.x == 0) scales[m] = sc.scale;
-    int8_t* q = codes + static_cast<size_t>(m) * ld;
-    for (int c = threadIdx.x; c < C; c += 512) q[c] = code1(value(c), sc);
+    int8_t* q = codes + m * ld;
+#pragma unroll 2
+    for (int c = threadIdx.x * VEC; c < C; c += 1024 * VEC) {
+        float v[VEC];
+        load(c, v);
+        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q + c) = codes8(v, sc);
+        else q[c] = code1(v[0], sc);
+    }
 }
 
 }  // namespace w4

@@ -104,8 +104,8 @@ def test_gemm_refusals(want, change):
 
 @pytest.mark.parametrize("want,change", [
     (1, dict(M=0)), (1, dict(w_s=None)), (1, dict(ldw=48)), (2, dict(K=131072, ldw=131072)),
-    (2, dict(tr=1, N=131072)), (3, dict(A=FAKE + 2)), (3, dict(w_s=FAKE + 4)), (4, dict()), (4, dict(ws=FAKE, nws=64)),
-    (3, dict(ws=FAKE + 8, nws=1 << 30))])
+    (2, dict(tr=1, N=131072)), (3, dict(A=FAKE + 2)), (3, dict(w_s=FAKE + 4)), (4, dict(M=40)),
+    (4, dict(M=40, ws=FAKE, nws=64)), (3, dict(M=40, ws=FAKE + 8, nws=1 << 30))])
 def test_linear_refusals(want, change):
     d = dict(A=FAKE, M=4, N=32, K=64, W=FAKE, ldw=64, w_s=FAKE, bias=None, tr=0, Y=FAKE, ws=None, nws=0, st=None)
     d.update(change)
