@@ -412,25 +412,78 @@ def w4_scatter_columns(A, idx, dst_cols: int, out=None):
     return out
 
 
-def _check_on(dev, *named):
-    """The other tensors of a call live where the first one does."""
-    for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+# The 8-bit layer's and the block norms' calls take a few microseconds of
+# device time on a few tokens, so their checks are first made as one chain of
+# cheap attribute tests; whatever fails there goes through the checks that say
+# what is wrong.
+class _Torch:
+    """torch and what the calls below use of it, looked up once."""
+    torch = None
+
+    @classmethod
+    def load(cls):
+        torch = _torch()
+        cls.bf16, cls.f32, cls.i8, cls.u8 = torch.bfloat16, torch.float32, torch.int8, torch.uint8
+        cls.empty_like = torch.empty_like
+        cls.get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        cls.stream = raw or (lambda idx: torch.cuda.current_stream(idx).cuda_stream)
+        cls.lib = library()
+        cls.torch = torch
 
 
-def _check_codes(t, name, rows=None, cols=None) -> int:
+def _call(name, dev, *args):
+    """The library call on device `dev` and its current stream."""
+    f = getattr(_Torch.lib, name)
+    if _Torch.get_device() == dev:
+        st = f(*args, _Torch.stream(dev))
+    else:
+        with _OnDevice(dev):
+            st = f(*args, _Torch.stream(dev))
+    if st != 0:
+        raise W4Error(st, name)
+
+
+def _check_rows(t, name, dtype, dev, shape):
+    """A dense tensor of this dtype and shape on CUDA device `dev`."""
+    if (t.__class__ is _Torch.torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        return
+    _check_cuda(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _check_first(t, name):
+    """The bf16 matrix that a call is about; returns its device's index."""
+    if _Torch.torch is None:
+        _Torch.load()
+    _check_cuda(t, name, _Torch.bf16)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.get_device()
+
+
+def _check_codes(t, name, dev=None, rows=None, cols=None) -> int:
     """Check int8 rows and return their stride in bytes, a multiple of 16 that
     covers a row rounded up to 16 (the layout :func:`w8_quantize_rows` gives)."""
-    torch = _torch()
+    if t.__class__ is _Torch.torch.Tensor and t.dtype is _Torch.i8 and t.dim() == 2 and t.get_device() == dev:
+        R, C = t.shape
+        ld, one = t.stride()
+        if R > 1 and C % 16 == 0 and one == 1 and ld % 16 == 0 and ld >= C and rows is None:
+            return ld
+    torch = _Torch.torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device (no CPU path exists)")
     if t.dtype != torch.int8:
         raise TypeError(f"{name} must be {torch.int8}, got {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dim() != 2 or (rows is not None and tuple(t.shape) != (rows, cols)):
+        raise ValueError(f"{name} must be 2-D{'' if rows is None else f' of shape {(rows, cols)}'}, "
+                         f"got {tuple(t.shape)}")
     R, C = t.shape
     need = (C + 15) // 16 * 16
     ld = t.stride(0) if R > 1 else need
@@ -441,10 +494,9 @@ def _check_codes(t, name, rows=None, cols=None) -> int:
     return ld
 
 
-def _empty_codes(R: int, C: int, dev):
-    torch = _torch()
+def _empty_codes(like, R: int, C: int):
     C16 = (C + 15) // 16 * 16
-    q = torch.empty((R, C16), dtype=torch.int8, device=dev)
+    q = like.new_empty((R, C16), dtype=_Torch.i8)
     return q if C16 == C else q[:, :C]
 
 
@@ -455,70 +507,51 @@ def w8_quantize_rows(X, channel_scales=None, out=None):
     The codes' rows start every multiple of 16 bytes (a view of a wider tensor
     when C is not one).  A row of zeros has scale 0, a row with an infinity or a
     NaN scale NaN and codes 0.  ``out``: (codes, scales) to write into."""
-    torch = _torch()
-    _check_cuda(X, "X", torch.bfloat16)
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D")
+    dev = _check_first(X, "X")
     R, C = X.shape
-    dev = X.device
     if channel_scales is not None:
-        _check_cuda(channel_scales, "channel_scales", torch.float32, (C,))
+        _check_rows(channel_scales, "channel_scales", _Torch.f32, dev, (C,))
     if out is None:
-        codes, scales = _empty_codes(R, C, dev), torch.empty((R,), dtype=torch.float32, device=dev)
+        codes, scales = _empty_codes(X, R, C), X.new_empty((R,), dtype=_Torch.f32)
         ld = (C + 15) // 16 * 16
     else:
         codes, scales = out
-        ld = _check_codes(codes, "codes", R, C)
-        _check_cuda(scales, "scales", torch.float32, (R,))
-    _check_on(dev, ("channel_scales", channel_scales), ("codes", codes), ("scales", scales))
-    with _OnDevice(dev) as on:
-        st = library().w8_quantize_rows(X.data_ptr(), R, C,
-                                        None if channel_scales is None else channel_scales.data_ptr(),
-                                        codes.data_ptr(), ld, scales.data_ptr(), _stream_ptr(on.idx))
-    if st != 0:
-        raise W4Error(st, "w8_quantize_rows")
+        ld = _check_codes(codes, "codes", dev, R, C)
+        _check_rows(scales, "scales", _Torch.f32, dev, (R,))
+    _call("w8_quantize_rows", dev, X.data_ptr(), R, C, _ptr(channel_scales), codes.data_ptr(), ld, scales.data_ptr())
     return codes, scales
 
 
-def _w8_product(fname, A, a_scales, lda, codes, scales, bias, transposed, out):
-    torch = _torch()
-    ldw = _check_codes(codes, "codes")
+def _w8_operands(A, dev, codes, scales, bias, transposed, out):
+    """Checks that w8a8_gemm and w8a8_linear share; returns (M, N, K, stride of the weights, output)."""
+    ldw = _check_codes(codes, "codes", dev)
     N, K = codes.shape
     in_len, out_len = (N, K) if transposed else (K, N)
-    if A.dim() != 2 or A.shape[1] != in_len:
-        raise ValueError(f"A must be 2-D with {in_len} columns, got {tuple(A.shape)}")
-    M = A.shape[0]
-    dev = A.device
+    M, got = A.shape
+    if got != in_len:
+        raise ValueError(f"A must have {in_len} columns, got {got}")
     if scales is not None:
-        _check_cuda(scales, "scales", torch.float32, (N,))
-    if a_scales is not None:
-        _check_cuda(a_scales, "a_scales", torch.float32, (M,))
+        _check_rows(scales, "scales", _Torch.f32, dev, (N,))
     if bias is not None:
-        _check_cuda(bias, "bias", torch.bfloat16, (out_len,))
+        _check_rows(bias, "bias", _Torch.bf16, dev, (out_len,))
     if out is None:
-        out = torch.empty((M, out_len), dtype=torch.bfloat16, device=dev)
+        out = A.new_empty((M, out_len), dtype=_Torch.bf16)
     else:
-        _check_cuda(out, "out", torch.bfloat16, (M, out_len))
-    _check_on(dev, ("codes", codes), ("scales", scales), ("a_scales", a_scales), ("bias", bias), ("out", out))
-    lib = library()
-    with _OnDevice(dev) as on:
-        key = (fname, on.idx, M, N, K, bool(transposed))
-        nws = _ws_cache.get(key)
-        if nws is None:
-            nws = int(getattr(lib, "w8a8_linear_workspace_bytes" if lda is None else "w8a8_workspace_bytes")(
-                M, N, K, int(bool(transposed))))
-            if len(_ws_cache) > 4096:
-                _ws_cache.clear()
-            _ws_cache[key] = nws
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-        head = (A.data_ptr(),) if lda is None else (A.data_ptr(), lda, a_scales.data_ptr())
-        st = getattr(lib, fname)(
-            *head, M, N, K, codes.data_ptr(), ldw, None if scales is None else scales.data_ptr(),
-            None if bias is None else bias.data_ptr(), int(bool(transposed)), out.data_ptr(),
-            None if ws is None else ws.data_ptr(), nws, _stream_ptr(on.idx))
-    if st != 0:
-        raise W4Error(st, fname)
-    return out
+        _check_rows(out, "out", _Torch.bf16, dev, (M, out_len))
+    return M, N, K, ldw, out
+
+
+def _w8_workspace(query, dev, M, N, K, transposed, like):
+    """Scratch of the size that the library asks for (a pure function of the shape and the device)."""
+    key = (query, dev, M, N, K, transposed)
+    n = _ws_cache.get(key)
+    if n is None:
+        with _OnDevice(dev):
+            n = int(getattr(_Torch.lib, query)(M, N, K, transposed))
+        if len(_ws_cache) > 4096:
+            _ws_cache.clear()
+        _ws_cache[key] = n
+    return (like.new_empty((n,), dtype=_Torch.u8) if n else None), n
 
 
 def w8a8_gemm(A, a_scales, codes, scales=None, *, bias=None, transposed: bool = False, out=None):
@@ -528,25 +561,39 @@ def w8a8_gemm(A, a_scales, codes, scales=None, *, bias=None, transposed: bool = 
     dX[m, k] = a_scales[m] sum_n A[m, n] codes[n, k] + bias[k], where A holds the rows of
     dY quantized with ``channel_scales=scales`` and ``scales`` is left out here.
     bf16 output; ``out`` may not overlap the inputs."""
-    if transposed and scales is not None:
+    if _Torch.torch is None:
+        _Torch.load()
+    tr = 1 if transposed else 0
+    if tr and scales is not None:
         raise ValueError("transposed: fold the weights' scales into A "
                          "(w8_quantize_rows with channel_scales) and pass scales=None")
-    if not transposed and scales is None:
+    if not tr and scales is None:
         raise ValueError("scales of the weights are needed")
     if a_scales is None:
         raise ValueError("a_scales are needed")
-    lda = _check_codes(A, "A")
-    return _w8_product("w8a8_gemm", A, a_scales, lda, codes, scales, bias, transposed, out)
+    dev = A.get_device() if isinstance(A, _Torch.torch.Tensor) and A.is_cuda else None
+    lda = _check_codes(A, "A", dev)
+    M, N, K, ldw, out = _w8_operands(A, dev, codes, scales, bias, tr, out)
+    _check_rows(a_scales, "a_scales", _Torch.f32, dev, (M,))
+    ws, nws = _w8_workspace("w8a8_workspace_bytes", dev, M, N, K, tr, out)
+    _call("w8a8_gemm", dev, A.data_ptr(), lda, a_scales.data_ptr(), M, N, K, codes.data_ptr(), ldw, _ptr(scales),
+          _ptr(bias), tr, out.data_ptr(), _ptr(ws), nws)
+    return out
 
 
 def w8a8_linear(A, codes, scales, *, bias=None, transposed: bool = False, out=None):
     """8-bit linear layer on bf16 rows: :func:`w8_quantize_rows` on A and
     :func:`w8a8_gemm` in one call.  Y = A . dequant(codes)^T (A [M, K]), or,
     transposed, dX = A . dequant(codes) (A [M, N]).  ``out`` may not overlap the inputs."""
-    _check_cuda(A, "A", _torch().bfloat16)
+    dev = _check_first(A, "A")
     if scales is None:
         raise ValueError("scales of the weights are needed")
-    return _w8_product("w8a8_linear", A, None, None, codes, scales, bias, transposed, out)
+    tr = 1 if transposed else 0
+    M, N, K, ldw, out = _w8_operands(A, dev, codes, scales, bias, tr, out)
+    ws, nws = _w8_workspace("w8a8_linear_workspace_bytes", dev, M, N, K, tr, out)
+    _call("w8a8_linear", dev, A.data_ptr(), M, N, K, codes.data_ptr(), ldw, scales.data_ptr(), _ptr(bias), tr,
+          out.data_ptr(), _ptr(ws), nws)
+    return out
 
 
 class BlockNorm(NamedTuple):
@@ -566,20 +613,23 @@ class BlockNormGrad(NamedTuple):
     d_gate: Any
 
 
-def _check_norm(rows, C, dev, pre_weight, post_weight, gate, y):
+def _check_norm(M, C, dev, pre_weight, post_weight, gate, y):
     """The norm's weights and gate; returns the C API's gate kind."""
-    torch = _torch()
-    _check_cuda(pre_weight, "pre_weight", torch.bfloat16, (C,))
-    if y is None and (post_weight is not None or gate is not None):
+    bf16 = _Torch.bf16
+    _check_rows(pre_weight, "pre_weight", bf16, dev, (C,))
+    if y is not None:
+        _check_rows(y, "y", bf16, dev, (M, C))
+    elif post_weight is not None or gate is not None:
         raise ValueError("post_weight and gate belong to y, which is not given")
     if post_weight is not None:
-        _check_cuda(post_weight, "post_weight", torch.bfloat16, (C,))
-    kind = 0
-    if gate is not None:
-        kind = 1 if isinstance(gate, torch.Tensor) and gate.dim() == 1 else 2
-        _check_cuda(gate, "gate", torch.bfloat16, (C,) if kind == 1 else (rows, C))
-    _check_on(dev, ("pre_weight", pre_weight), ("post_weight", post_weight), ("gate", gate))
-    return kind
+        _check_rows(post_weight, "post_weight", bf16, dev, (C,))
+    if gate is None:
+        return 0
+    if isinstance(gate, _Torch.torch.Tensor) and gate.dim() == 1:
+        _check_rows(gate, "gate", bf16, dev, (C,))
+        return 1
+    _check_rows(gate, "gate", bf16, dev, (M, C))
+    return 2
 
 
 def _ptr(t):
@@ -597,38 +647,26 @@ def w4_block_norm(x, y=None, *, pre_weight, post_weight=None, gate=None, residua
     w + weight_offset.  gate: bf16 [C] or [M, C].  ``quantize`` gives the normed rows as
     int8 codes and scales for :func:`w8a8_gemm` instead of bf16.  ``keep_rstd`` keeps what
     :func:`w4_block_norm_backward` needs.  ``residual_out`` may be x or y (in place)."""
-    torch = _torch()
-    _check_cuda(x, "x", torch.bfloat16)
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D")
+    dev = _check_first(x, "x")
     M, C = x.shape
-    dev = x.device
-    if y is not None:
-        _check_cuda(y, "y", torch.bfloat16, (M, C))
-    elif residual_out is not None:
-        raise ValueError("without y the residual is x itself")
     kind = _check_norm(M, C, dev, pre_weight, post_weight, gate, y)
-    residual = x
-    if y is not None:
-        if residual_out is None:
-            residual = torch.empty_like(x)
-        else:
-            _check_cuda(residual_out, "residual_out", torch.bfloat16, (M, C))
-            residual = residual_out
-    _check_on(dev, ("y", y), ("residual_out", residual))
-    scales = None
-    if quantize:
-        normed, scales = _empty_codes(M, C, dev), torch.empty((M,), dtype=torch.float32, device=dev)
+    if y is None:
+        if residual_out is not None:
+            raise ValueError("without y the residual is x itself")
+        residual = x
+    elif residual_out is None:
+        residual = _Torch.empty_like(x)
     else:
-        normed = torch.empty((M, C), dtype=torch.bfloat16, device=dev)
-    rstd = torch.empty((2, M), dtype=torch.float32, device=dev) if keep_rstd else None
-    with _OnDevice(dev) as on:
-        st = library().w4_block_norm(
-            x.data_ptr(), _ptr(y), M, C, _ptr(post_weight), _ptr(gate), kind, residual_scale,
-            pre_weight.data_ptr(), weight_offset, eps, None if y is None else residual.data_ptr(),
-            normed.data_ptr(), (C + 15) // 16 * 16, _ptr(scales), _ptr(rstd), _stream_ptr(on.idx))
-    if st != 0:
-        raise W4Error(st, "w4_block_norm")
+        _check_rows(residual_out, "residual_out", _Torch.bf16, dev, (M, C))
+        residual = residual_out
+    if quantize:
+        normed, scales = _empty_codes(x, M, C), x.new_empty((M,), dtype=_Torch.f32)
+    else:
+        normed, scales = _Torch.empty_like(x), None
+    rstd = x.new_empty((2, M), dtype=_Torch.f32) if keep_rstd else None
+    _call("w4_block_norm", dev, x.data_ptr(), _ptr(y), M, C, _ptr(post_weight), _ptr(gate), kind, residual_scale,
+          pre_weight.data_ptr(), weight_offset, eps, None if y is None else residual.data_ptr(), normed.data_ptr(),
+          (C + 15) // 16 * 16, _ptr(scales), _ptr(rstd))
     return BlockNorm(residual, normed, scales, rstd)
 
 
@@ -639,36 +677,28 @@ def w4_block_norm_backward(d_normed, residual, rstd, y=None, *, d_residual=None,
 
     All bf16: d_x, d_y [M, C], d_pre_weight, d_post_weight [C], d_gate in the gate's shape.
     Quantized rows count as the values they stand for.  The same inputs give the same bits."""
-    torch = _torch()
-    _check_cuda(d_normed, "d_normed", torch.bfloat16)
-    if d_normed.dim() != 2:
-        raise ValueError("d_normed must be 2-D")
+    dev = _check_first(d_normed, "d_normed")
     M, C = d_normed.shape
-    dev = d_normed.device
-    _check_cuda(residual, "residual", torch.bfloat16, (M, C))
-    _check_cuda(rstd, "rstd", torch.float32, (2, M))
+    bf16, empty_like = _Torch.bf16, _Torch.empty_like
+    _check_rows(residual, "residual", bf16, dev, (M, C))
+    _check_rows(rstd, "rstd", _Torch.f32, dev, (2, M))
     if d_residual is not None:
-        _check_cuda(d_residual, "d_residual", torch.bfloat16, (M, C))
-    if y is not None:
-        _check_cuda(y, "y", torch.bfloat16, (M, C))
+        _check_rows(d_residual, "d_residual", bf16, dev, (M, C))
     kind = _check_norm(M, C, dev, pre_weight, post_weight, gate, y)
-    _check_on(dev, ("residual", residual), ("rstd", rstd), ("d_residual", d_residual), ("y", y))
-    d_x = torch.empty_like(d_normed)
-    d_y = None if y is None else torch.empty_like(y)
-    d_pre = torch.empty_like(pre_weight)
-    d_post = None if post_weight is None else torch.empty_like(post_weight)
-    d_gate = None if gate is None else torch.empty_like(gate)
-    lib = library()
-    with _OnDevice(dev) as on:
-        nws = int(lib.w4_block_norm_workspace_bytes(M, C))
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-        st = lib.w4_block_norm_backward(
-            d_normed.data_ptr(), _ptr(d_residual), residual.data_ptr(), rstd.data_ptr(), _ptr(y), M, C,
-            _ptr(post_weight), _ptr(gate), kind, residual_scale, pre_weight.data_ptr(), weight_offset,
-            d_x.data_ptr(), _ptr(d_y), d_pre.data_ptr(), _ptr(d_post), _ptr(d_gate), ws.data_ptr(), nws,
-            _stream_ptr(on.idx))
-    if st != 0:
-        raise W4Error(st, "w4_block_norm_backward")
+    d_x = empty_like(d_normed)
+    d_y = None if y is None else empty_like(y)
+    d_pre = empty_like(pre_weight)
+    d_post = None if post_weight is None else empty_like(post_weight)
+    d_gate = None if gate is None else empty_like(gate)
+    key = ("norm", dev, M, C)
+    nws = _ws_cache.get(key)
+    if nws is None:
+        with _OnDevice(dev):
+            nws = _ws_cache[key] = int(_Torch.lib.w4_block_norm_workspace_bytes(M, C))
+    ws = d_x.new_empty((nws,), dtype=_Torch.u8)
+    _call("w4_block_norm_backward", dev, d_normed.data_ptr(), _ptr(d_residual), residual.data_ptr(), rstd.data_ptr(),
+          _ptr(y), M, C, _ptr(post_weight), _ptr(gate), kind, residual_scale, pre_weight.data_ptr(), weight_offset,
+          d_x.data_ptr(), _ptr(d_y), d_pre.data_ptr(), _ptr(d_post), _ptr(d_gate), ws.data_ptr(), nws)
     return BlockNormGrad(d_x, d_y, d_pre, d_post, d_gate)
 
 
