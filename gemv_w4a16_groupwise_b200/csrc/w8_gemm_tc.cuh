@@ -17,7 +17,7 @@
 // borders.  A tile cut that way leaves int32 partials (exact, so their order
 // does not matter) which w8_finalize_kernel adds, scales and rounds.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (in the pair's first CTA), 2..5
+// Warps: 0 TMA producer, 1 MMA issuer (in the pair's first CTA), 2..9
 // epilogue.  Accumulators are double buffered, so a tile's epilogue runs
 // beside the next tile's products.  Full barriers live in the first CTA and
 // count both CTAs' bytes; the stage's release and the accumulator's
@@ -33,10 +33,13 @@ namespace w4 {
 constexpr int kW8Rows = 256;          // outputs of a pair's tile
 constexpr int kW8Red = 128;           // reduction of a stage
 constexpr int kW8ABytes = 128 * kW8Red;
-constexpr int kW8EpiWarps = 4;
+constexpr int kW8EpiWarps = 8;
 constexpr int kW8Threads = 64 + 32 * kW8EpiWarps;
-constexpr int kW8StageTokens = 32;    // tokens an epilogue warp stages at a time
-constexpr int kW8EpiBytes = kW8EpiWarps * kW8StageTokens * 32 * 2;
+// An epilogue warp stages 32 outputs of 16 token pairs, the pairs 36 words
+// apart (two pairs' 16-byte reads then meet no bank twice), and 32 scales.
+constexpr int kW8PairStride = 36;
+constexpr int kW8EpiWarpBytes = 16 * kW8PairStride * 4 + 32 * 4;
+constexpr int kW8EpiBytes = kW8EpiWarps * kW8EpiWarpBytes;
 
 __host__ __device__ constexpr int w8_stage_bytes(int TN) { return kW8ABytes + TN / 2 * kW8Red; }
 
@@ -283,57 +286,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         }
     } else {
         // ------------------------------------------------ epilogue
+        // Two warps per quadrant of 32 TMEM lanes (outputs), each on half of
+        // the tile's tokens, 32 at a time.
         const int q = warp & 3;                 // TMEM lanes 32 q .. 32 q + 31
-        uint16_t* stage = reinterpret_cast<uint16_t*>(epi) + (warp - 2) * kW8StageTokens * 32;
+        const int half = (warp - 2) >> 2;
+        constexpr int kBlocks = TN >= 64 ? TN / 64 : 1;
+        const int cbase = half * kBlocks * 32;  // TN = 32: the second half has nothing
+        uint32_t* stage = reinterpret_cast<uint32_t*>(epi + (warp - 2) * kW8EpiWarpBytes);
+        float* scales = reinterpret_cast<float*>(stage + 16 * kW8PairStride);
         int i = 0;
         while (walk.next(&u)) {
             const int buf = i & 1;
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, abort_flag,
-                                                                      kErrTimeoutAccum));
-            if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) break;
-            tc_fence_after();
-            const int m0 = (u.tile % a.tiles_m) * TN;
+            const int m0 = (u.tile % a.tiles_m) * TN + cbase;
             const int row = static_cast<int>(rank) * 128 + 32 * q + lane;      // in the tile
             const int o0 = (u.tile / a.tiles_m) * kW8Rows;
             const int o = o0 + row;
             const bool ov = o < out;
-            const uint32_t acc = tmem_d + static_cast<uint32_t>(buf) * TN + (static_cast<uint32_t>(32 * q) << 16);
+            // scales and bias come in while the products still run
             const float ws = (!TR && ov) ? a.p.w_scales[o] : 1.0f;
             const float bias = (a.p.bias && ov) ? bf16_bits_to_float(a.p.bias[o]) : 0.0f;
-            const int tokens = min(TN, a.p.M - m0);
-#pragma unroll 1
-            for (int c0 = 0; c0 < tokens; c0 += 32) {
+            const int tokens = cbase < TN ? min(kBlocks * 32, a.p.M - m0) : 0;
+            float as[kBlocks];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+                as[b] = 32 * b + lane < tokens ? a.p.a_scales[m0 + 32 * b + lane] : 0.0f;
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, abort_flag,
+                                                                      kErrTimeoutAccum));
+            if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) break;
+            tc_fence_after();
+            const uint32_t acc =
+                tmem_d + static_cast<uint32_t>(buf * TN + cbase) + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                if (32 * b >= tokens) break;
                 uint32_t r[32];
                 __syncwarp();
-                tmem_ld_x32(acc + static_cast<uint32_t>(c0), r);
+                tmem_ld_x32(acc + static_cast<uint32_t>(32 * b), r);
                 if (u.part >= 0) {
-                    int32_t* pt = a.part + (static_cast<size_t>(u.part) * TN + c0) * kW8Rows + row;
+                    int32_t* pt = a.part + (static_cast<size_t>(u.part) * TN + cbase + 32 * b) * kW8Rows + row;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) pt[e * kW8Rows] = static_cast<int32_t>(r[e]);
                     continue;
                 }
-                const float as = (m0 + c0 + lane < a.p.M) ? a.p.a_scales[m0 + c0 + lane] : 0.0f;
-                if ((out & 7) == 0) {
-                    // through shared memory: [token][32 outputs], then 16 bytes a lane
+                scales[lane] = as[b];
+                __syncwarp();
+                // pairs of tokens as bf16x2
+                uint32_t y[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        stage[e * 32 + lane] = w8_output(static_cast<int>(r[e]),
-                                                         __shfl_sync(0xFFFFFFFFu, as, e) * ws, bias);
+                for (int e = 0; e < 16; ++e) {
+                    const float2 sc = *reinterpret_cast<const float2*>(scales + 2 * e);
+                    y[e] = bf162_bits(__floats2bfloat162_rn(
+                        fmaf(static_cast<float>(static_cast<int>(r[2 * e])), sc.x * ws, bias),
+                        fmaf(static_cast<float>(static_cast<int>(r[2 * e + 1])), sc.y * ws, bias)));
+                }
+                const int mb = m0 + 32 * b;
+                if ((out & 7) == 0) {
+                    // through shared memory: [token pair][output], then 8 outputs of two tokens a lane
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) stage[e * kW8PairStride + lane] = y[e];
                     __syncwarp();
                     const int ol = o0 + static_cast<int>(rank) * 128 + 32 * q + (lane & 3) * 8;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int t = g * 8 + (lane >> 2);
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + t * 32 + (lane & 3) * 8);
-                        if (m0 + c0 + t < a.p.M && ol < out)
-                            *reinterpret_cast<uint4*>(a.p.Y + static_cast<size_t>(m0 + c0 + t) * out + ol) = v;
+                    for (int g = 0; g < 2; ++g) {
+                        const int pr = g * 8 + (lane >> 2), m = mb + 2 * pr;
+                        const uint32_t* src = stage + pr * kW8PairStride + (lane & 3) * 8;
+                        const uint4 v0 = *reinterpret_cast<const uint4*>(src);
+                        const uint4 v1 = *reinterpret_cast<const uint4*>(src + 4);
+                        uint16_t* dst = a.p.Y + static_cast<size_t>(m) * out + ol;
+                        if (m < a.p.M && ol < out)
+                            *reinterpret_cast<uint4*>(dst) =
+                                make_uint4(prmt(v0.x, v0.y, 0x5410u), prmt(v0.z, v0.w, 0x5410u),
+                                           prmt(v1.x, v1.y, 0x5410u), prmt(v1.z, v1.w, 0x5410u));
+                        if (m + 1 < a.p.M && ol < out)
+                            *reinterpret_cast<uint4*>(dst + out) =
+                                make_uint4(prmt(v0.x, v0.y, 0x7632u), prmt(v0.z, v0.w, 0x7632u),
+                                           prmt(v1.x, v1.y, 0x7632u), prmt(v1.z, v1.w, 0x7632u));
                     }
-                    __syncwarp();
                 } else {
+                    uint16_t* dst = a.p.Y + static_cast<size_t>(mb) * out + o;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint16_t y = w8_output(static_cast<int>(r[e]), __shfl_sync(0xFFFFFFFFu, as, e) * ws, bias);
-                        if (m0 + c0 + e < a.p.M && ov) a.p.Y[static_cast<size_t>(m0 + c0 + e) * out + o] = y;
+                    for (int e = 0; e < 16; ++e) {
+                        if (ov && mb + 2 * e < a.p.M) dst[static_cast<size_t>(2 * e) * out] = static_cast<uint16_t>(y[e]);
+                        if (ov && mb + 2 * e + 1 < a.p.M)
+                            dst[static_cast<size_t>(2 * e + 1) * out] = static_cast<uint16_t>(y[e] >> 16);
                     }
                 }
             }
