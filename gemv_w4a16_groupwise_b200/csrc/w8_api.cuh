@@ -96,7 +96,8 @@ bool make_map_i8(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols
 }
 
 template <bool TR, int TN>
-w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, const DeviceInfo& di, cudaStream_t st) {
+w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, bool early, const DeviceInfo& di,
+                       cudaStream_t st) {
     constexpr int kStage = w4::w8_stage_bytes(TN);
     const size_t fixed = 1024 + w4::kW8EpiBytes + 128;
     const int stages = std::min(10, static_cast<int>((di.max_smem_optin - fixed) / (kStage + 16)));
@@ -108,12 +109,11 @@ w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, cons
         return W4_ERR_CUDA;
     auto fn = w4::w8_gemm_tc_kernel<TR, TN>;
     if (ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
-    const w4::W8TcArgs a = {g, part, p.tiles_m, p.tiles, p.F, p.chunks, p.cut_pairs, stages};
+    const w4::W8TcArgs a = {g, part, p.tiles_m, p.tiles, p.F, p.chunks, p.cut_pairs, stages, early ? 1 : 0};
     launch_pdl(fn, dim3(2 * p.grid_pairs), dim3(w4::kW8Threads), smem, st, wmap, amap, a);
     const w4_status s = launch_status();
     if (s != W4_OK || p.ws == 0) return s;
-    const long long threads = static_cast<long long>(p.tiles - p.F) * TN * (w4::kW8Rows / 4);
-    launch_pdl(w4::w8_finalize_kernel<TR>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, st, a, TN);
+    launch_pdl(w4::w8_finalize_kernel<TR>, dim3(TN * (w4::kW8Rows / 4) / 256, p.tiles - p.F), dim3(256), 0, st, a, TN);
     return launch_status();
 }
 
@@ -142,16 +142,27 @@ w4_status launch_w8_gemv(const w4::W8Args& p, const uint16_t* X, cudaStream_t st
     return launch_status();
 }
 
-w4_status run_w8_gemm(const w4::W8Args& a, bool transposed, void* ws, cudaStream_t st) {
+// `early`: the kernel launched just before on the stream is run_quantize_rows,
+// which does not write the weights and lets its dependents start only after
+// all that came before it.
+w4_status run_w8_gemm(const w4::W8Args& a, bool transposed, void* ws, bool early, cudaStream_t st) {
     if (w8_gemv_serves(a.M, transposed)) return launch_w8_gemv<0>(a, nullptr, st);
     const DeviceInfo di = device_info(current_device());
     const W8Plan p = plan_w8(a.M, a.N, a.K, transposed, di.sms);
     int32_t* part = static_cast<int32_t*>(ws);
     switch (p.TN) {
-        case 32: return transposed ? launch_w8_tc<true, 32>(p, a, part, di, st) : launch_w8_tc<false, 32>(p, a, part, di, st);
-        case 64: return transposed ? launch_w8_tc<true, 64>(p, a, part, di, st) : launch_w8_tc<false, 64>(p, a, part, di, st);
-        case 128: return transposed ? launch_w8_tc<true, 128>(p, a, part, di, st) : launch_w8_tc<false, 128>(p, a, part, di, st);
-        default: return transposed ? launch_w8_tc<true, 256>(p, a, part, di, st) : launch_w8_tc<false, 256>(p, a, part, di, st);
+        case 32:
+            return transposed ? launch_w8_tc<true, 32>(p, a, part, early, di, st)
+                              : launch_w8_tc<false, 32>(p, a, part, early, di, st);
+        case 64:
+            return transposed ? launch_w8_tc<true, 64>(p, a, part, early, di, st)
+                              : launch_w8_tc<false, 64>(p, a, part, early, di, st);
+        case 128:
+            return transposed ? launch_w8_tc<true, 128>(p, a, part, early, di, st)
+                              : launch_w8_tc<false, 128>(p, a, part, early, di, st);
+        default:
+            return transposed ? launch_w8_tc<true, 256>(p, a, part, early, di, st)
+                              : launch_w8_tc<false, 256>(p, a, part, early, di, st);
     }
 }
 
@@ -194,7 +205,7 @@ w4_status w8a8_gemm(const int8_t* A, long long lda, const float* a_scales, int M
     if (!aligned16(workspace)) return W4_ERR_ALIGNMENT;
     const w4::W8Args a = {A, a_scales, W, w_scales, static_cast<const uint16_t*>(bias),
                           static_cast<uint16_t*>(Y), lda, ldw, M, N, K};
-    return run_w8_gemm(a, transposed != 0, workspace, static_cast<cudaStream_t>(stream));
+    return run_w8_gemm(a, transposed != 0, workspace, false, static_cast<cudaStream_t>(stream));
 }
 
 w4_status w8a8_linear(const void* A, int M, int N, int K, const int8_t* W, long long ldw, const float* w_scales,
@@ -223,7 +234,8 @@ w4_status w8a8_linear(const void* A, int M, int N, int K, const int8_t* W, long 
     if (q != W4_OK) return q;
     const w4::W8Args a = {codes, scales, W, transposed ? nullptr : w_scales, static_cast<const uint16_t*>(bias),
                           static_cast<uint16_t*>(Y), static_cast<long long>(ld), ldw, M, N, K};
-    return run_w8_gemm(a, transposed != 0, reinterpret_cast<uint8_t*>(scales) + round16(M * sizeof(float)), st);
+    return run_w8_gemm(a, transposed != 0, reinterpret_cast<uint8_t*>(scales) + round16(M * sizeof(float)), true,
+                       st);
 }
 
 }  // extern "C"

@@ -51,6 +51,7 @@ struct W8TcArgs {
     int chunks;          // stages of one tile
     int cut_pairs;       // pairs that share the tiles from F on
     int stages;
+    int early;           // the kernel before does not write the weights
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -126,7 +127,7 @@ struct W8Unit {
 struct W8Walk {
     int p, P, F, chunks;
     int next_whole;
-    long long c, c1;     // the pair's share of the cut tiles' stages
+    uint32_t c, c1;      // the pair's share of the cut tiles' stages (< 2^10 pairs x 2^10 stages, squared at most 2^31)
     int cut_units;
     __device__ W8Walk(const W8TcArgs& a, int pair, int pairs) {
         p = pair;
@@ -134,7 +135,7 @@ struct W8Walk {
         F = a.F;
         chunks = a.chunks;
         next_whole = pair;
-        const long long total = pair < a.cut_pairs ? static_cast<long long>(a.tiles - a.F) * a.chunks : 0;
+        const uint32_t total = pair < a.cut_pairs ? static_cast<uint32_t>(a.tiles - a.F) * a.chunks : 0u;
         c = total * pair / a.cut_pairs;
         c1 = total * (pair + 1) / a.cut_pairs;
         cut_units = 0;
@@ -148,8 +149,8 @@ struct W8Walk {
         if (c >= c1) return false;
         const int t = static_cast<int>(c / chunks);
         u->tile = F + t;
-        u->kb0 = static_cast<int>(c - static_cast<long long>(t) * chunks);
-        u->kb1 = static_cast<int>(min(static_cast<long long>(chunks), u->kb0 + (c1 - c)));
+        u->kb0 = static_cast<int>(c) - t * chunks;
+        u->kb1 = min(chunks, u->kb0 + static_cast<int>(c1 - c));
         u->part = (u->kb0 == 0 && u->kb1 == chunks) ? -1 : 2 * p + (cut_units > 0 ? 1 : 0);
         ++cut_units;
         c += u->kb1 - u->kb0;
@@ -208,30 +209,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
     tc_fence_after();
     const uint32_t tmem_d = *tmem_slot;
     pdl_launch_dependents();
-    pdl_wait();
 
     W8Walk walk(a, pair, pairs);
     W8Unit u;
+    auto load_weights = [&](int s, int kb, int o0) {
+        uint8_t* st = base + s * kStageBytes;
+        const uint32_t bar = first_cta_addr(&full[s]);
+        if (TR) tma_load_2d_pair(st, &wmap, o0, kb * kW8Red, bar);
+        else tma_load_2d_pair(st, &wmap, kb * kW8Red, o0, bar);
+    };
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         if (lane == 0) {
             int s = 0;
             uint32_t round = 0;
             bool ok = true;
+            // Weights that no kernel still running writes (a.early) are asked
+            // for before the tokens' codes are waited for: the first NS stages.
+            int early = 0;
+            if (a.early) {
+                W8Walk ahead(a, pair, pairs);
+                while (early < NS && ahead.next(&u)) {
+                    const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
+                    for (int kb = u.kb0; kb < u.kb1 && early < NS; ++kb, ++early) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[early], 2 * kStageBytes);
+                        load_weights(early, kb, o0);
+                    }
+                }
+            }
+            pdl_wait();
+            int n = 0;
             while (ok && walk.next(&u)) {
                 const int m0 = (u.tile % a.tiles_m) * TN + static_cast<int>(rank) * (TN / 2);
                 const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
-                for (int kb = u.kb0; kb < u.kb1; ++kb) {
+                for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
                     if (round > 0 && !mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* st = base + s * kStageBytes;
-                    const uint32_t bar = first_cta_addr(&full[s]);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                    if (TR) tma_load_2d_pair(st, &wmap, o0, kb * kW8Red, bar);
-                    else tma_load_2d_pair(st, &wmap, kb * kW8Red, o0, bar);
-                    tma_load_2d_pair(st + kW8ABytes, &amap, kb * kW8Red, m0, bar);
+                    if (n >= early) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                        load_weights(s, kb, o0);
+                    }
+                    tma_load_2d_pair(base + s * kStageBytes + kW8ABytes, &amap, kb * kW8Red, m0,
+                                     first_cta_addr(&full[s]));
                     if (++s == NS) {
                         s = 0;
                         ++round;
@@ -295,6 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         uint32_t* stage = reinterpret_cast<uint32_t*>(epi + (warp - 2) * kW8EpiWarpBytes);
         float* scales = reinterpret_cast<float*>(stage + 16 * kW8PairStride);
         int i = 0;
+        pdl_wait();
         while (walk.next(&u)) {
             const int buf = i & 1;
             const int m0 = (u.tile % a.tiles_m) * TN + cbase;
@@ -403,34 +425,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
 }
 
 // The cut tiles: Y = bf16(sum of the partials * scales + bias).  One thread
-// per token and four outputs; a tile that one pair computed whole is already
-// stored.  The pair whose share [total p / P, total (p + 1) / P) holds stage c
-// is ((c + 1) P - 1) / total.
+// per token and four outputs, blocks (x, y): 256 threads of tile F + y; a tile
+// that one pair computed whole is already stored.  The pair whose share
+// [total p / P, total (p + 1) / P) holds stage c is ((c + 1) P - 1) / total.
 template <bool TR>
 __global__ void __launch_bounds__(256) w8_finalize_kernel(const W8TcArgs a, int TN) {
     pdl_launch_dependents();
     pdl_wait();
-    const int pairs = a.cut_pairs;
+    const uint32_t pairs = a.cut_pairs;
     const int out = TR ? a.p.K : a.p.N;
-    const int per_tile = TN * (kW8Rows / 4);
-    const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    const int tt = static_cast<int>(idx / per_tile);
-    if (tt >= a.tiles - a.F) return;
-    const int e = static_cast<int>(idx - static_cast<long long>(tt) * per_tile);
+    const int tt = blockIdx.y, t = a.F + tt;
+    const int e = blockIdx.x * 256 + threadIdx.x;
     const int tok = e / (kW8Rows / 4), rl = (e % (kW8Rows / 4)) * 4;
-    const int t = a.F + tt;
     const int m = (t % a.tiles_m) * TN + tok, o = (t / a.tiles_m) * kW8Rows + rl;
     if (m >= a.p.M || o >= out) return;
-    const long long total = static_cast<long long>(a.tiles - a.F) * a.chunks;
-    const long long first = static_cast<long long>(tt) * a.chunks;
-    const int p0 = static_cast<int>(((first + 1) * pairs - 1) / total);
-    const int p1 = static_cast<int>(((first + a.chunks) * pairs - 1) / total);
+    const uint32_t total = static_cast<uint32_t>(a.tiles - a.F) * a.chunks;
+    const uint32_t first = static_cast<uint32_t>(tt) * a.chunks;
+    const uint32_t p0 = ((first + 1) * pairs - 1) / total;
+    const uint32_t p1 = ((first + a.chunks) * pairs - 1) / total;
     if (p0 == p1) return;
     int4 s = make_int4(0, 0, 0, 0);
-    for (int p = p0; p <= p1; ++p) {
-        // the pair's first unit lies in this tile, or in an earlier one
-        const bool first_unit = total * p / pairs >= first;
-        const int slot = 2 * p + (first_unit ? 0 : 1);
+#pragma unroll 4
+    for (uint32_t p = p0; p <= p1; ++p) {
+        // only the first of the pairs can have begun in an earlier tile
+        const uint32_t slot = 2 * p + (p == p0 && total * p / pairs < first ? 1 : 0);
         const int4 v = *reinterpret_cast<const int4*>(a.part + (static_cast<size_t>(slot) * TN + tok) * kW8Rows + rl);
         s.x += v.x;
         s.y += v.y;
