@@ -42,78 +42,109 @@ struct NormArgs {
     float alpha, off, eps;
 };
 
-template <int T, int V, int VEC, bool CODES>
-__global__ void __launch_bounds__(T) block_norm_kernel(const NormArgs a) {
-    using S = RowSpan<T, V, VEC>;
-    __shared__ float buf[2][32];
-    __shared__ uint32_t ubuf[32];
+// A block walks over rows blockIdx.x, + gridDim.x, ... with the next row's
+// loads under way while it works on one.  The values are worked on in pairs
+// (f32x2): with scalar arithmetic and predicated sums the kernel was bound by
+// the instructions it issued, not by memory.
+template <int T, int G, int VEC, bool CODES>
+__global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs a) {
+    using S = RowSpan<T, G, VEC>;
+    extern __shared__ uint4 ring[];
+    __shared__ float buf[2][2][32];      // [row's parity][reduction]
+    __shared__ uint32_t ubuf[2][32];
     const float inv_c = 1.0f / static_cast<float>(a.C);
-    const long long m = blockIdx.x;
-    const size_t at = static_cast<size_t>(m) * a.C;
+    const bool post = a.post != nullptr, token = a.gate_kind == kGateToken, gated = a.gate_kind != kGateNone;
+    const RowPipe<T, G, VEC, VEC == 8> pipe = {ring, 1 + (a.y ? 1 : 0) + (token ? 1 : 0), a.C};
     pdl_launch_dependents();
     pdl_wait();
-    uint32_t r[S::W];
-    S::load(r, a.x + at, a.C);
-    float rstd_y = 0.0f;
-    if (a.y) {
-        uint32_t y[S::W], w[S::W], g[S::W];
-        S::load(y, a.y + at, a.C);
-        if (a.post) {
-            S::load(w, a.post, a.C);
-            float ss = 0.0f;
+    auto fetch = [&](int stage, long long m) {
+        const size_t at = static_cast<size_t>(m) * a.C;
+        pipe.fetch(stage, 0, a.x + at);
+        if (a.y) pipe.fetch(stage, 1, a.y + at);
+        if (token) pipe.fetch(stage, 2, a.gate + at);
+        pipe.commit();
+    };
+    fetch(0, blockIdx.x);
+    const float2 off = both(a.off);
+    uint4 wpre[G];
 #pragma unroll
-            for (int e = 0; e < S::E; ++e) ss = fmaf(S::get(y, e), S::get(y, e), ss);
-            rstd_y = 1.0f / sqrtf(block_sum<T>(ss, buf[0]) * inv_c + a.eps);
-        }
-        if (a.gate_kind != kGateNone) S::load(g, a.gate + (a.gate_kind == kGateToken ? at : 0), a.C);
+    for (int g = 0; g < G; ++g) wpre[g] = S::load(a.pre, g, a.C);
+    int turn = 0;
+    for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+        const size_t at = static_cast<size_t>(m) * a.C;
+        const bool more = m + gridDim.x < a.M;
+        if (more) fetch(turn ^ 1, m + gridDim.x);
+        pipe.wait(more);
+        float rstd_y = 0.0f;
+        if (post) {
+            float2 ss = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) {
-            float t = S::get(y, e);
-            if (a.post) t = t * rstd_y * (S::get(w, e) + a.off);
-            if (a.gate_kind != kGateNone) t *= S::get(g, e);
-            S::put(r, e, to_bf16_bits(fmaf(a.alpha, t, S::get(r, e))));
-        }
-        S::store(r, a.residual + at, a.C);
-    }
-    uint32_t w[S::W];
-    S::load(w, a.pre, a.C);
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < S::E; ++e)
-        if (S::col(e / VEC) < a.C) ss = fmaf(S::get(r, e), S::get(r, e), ss);
-    const float rstd = 1.0f / sqrtf(block_sum<T>(ss, buf[1]) * inv_c + a.eps);
-    if (a.rstd && threadIdx.x == 0) {
-        a.rstd[m] = rstd_y;
-        a.rstd[a.M + m] = rstd;
-    }
-    auto normed = [&](int e) { return S::get(r, e) * rstd * (S::get(w, e) + a.off); };
-    if constexpr (!CODES) {
-#pragma unroll
-        for (int e = 0; e < S::E; ++e) S::put(r, e, to_bf16_bits(normed(e)));
-        S::store(r, static_cast<uint16_t*>(a.normed) + at, a.C);
-    } else {
-        // columns past C hold zeros in r, so they are neutral here
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < S::E; ++e)
-            if (S::col(e / VEC) < a.C) top = max(top, abs_bits(normed(e)));
-        top = block_max_bits<T>(top, ubuf);
-        const RowScale sc = row_scale(__uint_as_float(top));
-        if (threadIdx.x == 0) a.scales[m] = sc.scale;
-        int8_t* q = static_cast<int8_t*>(a.normed) + static_cast<size_t>(m) * a.ld;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = S::col(j);
-            if (c < a.C) {
-                if constexpr (VEC == 8) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = normed(8 * j + i);
-                    *reinterpret_cast<uint2*>(q + c) = codes8(v, sc);
-                } else {
-                    q[c] = code1(normed(j), sc);
+            for (int g = 0; g < G; ++g) {
+                const uint4 y = pipe.read(turn, 1, a.y + at, g);
+                for (uint32_t w : {y.x, y.y, y.z, y.w}) {
+                    const float2 v = unpack_bf16x2(w);
+                    ss = ffma2(v, v, ss);
                 }
             }
+            rstd_y = 1.0f / sqrtf(block_sum<T>(ss, buf[turn][0]) * inv_c + a.eps);
+        }
+        uint32_t r[G][4];
+        float2 ss = both(0.0f);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint4 x = pipe.read(turn, 0, a.x + at, g);
+            r[g][0] = x.x, r[g][1] = x.y, r[g][2] = x.z, r[g][3] = x.w;
+            if (a.y) {
+                const uint4 y = pipe.read(turn, 1, a.y + at, g);
+                float2 t[4] = {unpack_bf16x2(y.x), unpack_bf16x2(y.y), unpack_bf16x2(y.z), unpack_bf16x2(y.w)};
+                if (post) {
+                    const uint4 p = S::load(a.post, g, a.C);
+                    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        t[i] = fmul2(fmul2(t[i], both(rstd_y)), fadd2(unpack_bf16x2(w[i]), off));
+                }
+                if (gated) {
+                    const uint4 p = token ? pipe.read(turn, 2, a.gate + at, g) : S::load(a.gate, g, a.C);
+                    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t[i] = fmul2(t[i], unpack_bf16x2(w[i]));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[g][i] = pack_bf16x2(ffma2(both(a.alpha), t[i], unpack_bf16x2(r[g][i])));
+                S::store(a.residual + at, g, a.C, r[g]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = unpack_bf16x2(r[g][i]);
+                ss = ffma2(v, v, ss);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(block_sum<T>(ss, buf[turn][1]) * inv_c + a.eps);
+        if (a.rstd && threadIdx.x == 0) {
+            a.rstd[m] = rstd_y;
+            a.rstd[a.M + m] = rstd;
+        }
+        float2 n[G][4];
+        float top = 0.0f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint32_t w[4] = {wpre[g].x, wpre[g].y, wpre[g].z, wpre[g].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                n[g][i] = fmul2(fmul2(unpack_bf16x2(r[g][i]), both(rstd)), fadd2(unpack_bf16x2(w[i]), off));
+                if constexpr (CODES) top = max_abs(top, n[g][i]);
+                else r[g][i] = pack_bf16x2(n[g][i]);
+            }
+            if constexpr (!CODES) S::store(static_cast<uint16_t*>(a.normed) + at, g, a.C, r[g]);
+        }
+        if constexpr (CODES) {
+            const RowScale sc = row_scale(__uint_as_float(block_max_bits<T>(__float_as_uint(top), ubuf[turn])));
+            if (threadIdx.x == 0) a.scales[m] = sc.scale;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                store_codes<S, VEC>(static_cast<int8_t*>(a.normed) + static_cast<size_t>(m) * a.ld, g, a.C,
+                                    codes8(n[g], sc));
         }
     }
 }
@@ -135,144 +166,220 @@ struct NormGradArgs {
     float alpha, off;
 };
 
+// Blocks an SM holds: 512 threads' worth at two groups (128 registers each),
+// 768 at one.
+__host__ __device__ constexpr int norm_grad_blocks_per_sm(int T, int G) {
+    return T == 1024 ? 1 : G == 2 ? 512 / T : 768 / T;
+}
+
 // One block takes rows blockIdx.x, + gridDim.x, ...; a thread keeps the same
 // columns throughout and with them the column sums of the weight gradients,
-// in registers, or in shared memory (ACC_SMEM) where 1024 threads leave no
-// room for them.
-template <int T, int V, int VEC, bool ACC_SMEM>
-__global__ void __launch_bounds__(T) block_norm_backward_kernel(const NormGradArgs a) {
-    using S = RowSpan<T, V, VEC>;
-    extern __shared__ float acc_smem[];     // [sums][E][T] with ACC_SMEM
-    __shared__ float buf[4][32];
+// in registers, or in shared memory (ACC_SMEM, then without the row pipe)
+// where 1024 threads leave no room for them.  What a reduction separates is
+// read again from the pipe instead of being held.
+template <int T, int G, int VEC, bool ACC_SMEM>
+__global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_backward_kernel(const NormGradArgs a) {
+    using S = RowSpan<T, G, VEC>;
+    constexpr bool PIPED = VEC == 8 && !ACC_SMEM;
+    constexpr int kRegs = ACC_SMEM ? 1 : G;
+    extern __shared__ uint4 dyn_smem[];     // the row pipe; with ACC_SMEM the sums, [sums][G][4][T]
+    float2* acc_smem = reinterpret_cast<float2*>(dyn_smem);
+    __shared__ float buf[2][2][32];
     const float inv_c = 1.0f / static_cast<float>(a.C);
+    const bool post = a.post != nullptr, chan = a.gate_kind == kGateChannel, token = a.gate_kind == kGateToken;
     pdl_launch_dependents();
     pdl_wait();
-    float acc_pre[ACC_SMEM ? 1 : S::E], acc_post[ACC_SMEM ? 1 : S::E], acc_gate[ACC_SMEM ? 1 : S::E];
-    const bool post = a.post != nullptr, chan = a.gate_kind == kGateChannel;
+    float2 acc_pre[kRegs][4], acc_post[kRegs][4], acc_gate[kRegs][4];
+    const int sums = 1 + (post ? 1 : 0) + (chan ? 1 : 0);
+    if constexpr (ACC_SMEM) {
+        for (int e = 0; e < sums * G * 4; ++e) acc_smem[e * T + threadIdx.x] = both(0.0f);
+    } else {
 #pragma unroll
-    for (int e = 0; e < S::E; ++e) {
-        if constexpr (ACC_SMEM) {
-            acc_smem[e * T + threadIdx.x] = 0.0f;
-            if (post) acc_smem[(S::E + e) * T + threadIdx.x] = 0.0f;
-            if (chan) acc_smem[((post ? 2 : 1) * S::E + e) * T + threadIdx.x] = 0.0f;
-        } else {
-            acc_pre[e] = acc_post[e] = acc_gate[e] = 0.0f;
-        }
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc_pre[g][i] = acc_post[g][i] = acc_gate[g][i] = both(0.0f);
     }
-    auto add = [&](float (&reg)[ACC_SMEM ? 1 : S::E], int slot, int e, float v) {
-        if constexpr (ACC_SMEM) acc_smem[(slot * S::E + e) * T + threadIdx.x] += v;
-        else reg[e] += v;
+    auto add = [&](float2 (&reg)[kRegs][4], int slab, int g, int i, float2 x, float2 y) {
+        if constexpr (ACC_SMEM) {
+            float2& s = acc_smem[((slab * G + g) * 4 + i) * T + threadIdx.x];
+            s = ffma2(x, y, s);
+        } else {
+            reg[g][i] = ffma2(x, y, reg[g][i]);
+        }
     };
-    uint32_t wpre[S::W];
-    S::load(wpre, a.pre, a.C);
+    const int dres_at = 2, y_at = 2 + (a.dres ? 1 : 0), gate_at = y_at + (a.y ? 1 : 0);
+    const RowPipe<T, G, VEC, PIPED> pipe = {dyn_smem, gate_at + (token ? 1 : 0), a.C};
+    auto fetch = [&](int stage, long long m) {
+        const size_t at = static_cast<size_t>(m) * a.C;
+        pipe.fetch(stage, 0, a.dn + at);
+        pipe.fetch(stage, 1, a.r + at);
+        if (a.dres) pipe.fetch(stage, dres_at, a.dres + at);
+        if (a.y) pipe.fetch(stage, y_at, a.y + at);
+        if (token) pipe.fetch(stage, gate_at, a.gate + at);
+        pipe.commit();
+    };
+    auto words = [](uint4 v, uint32_t (&w)[4]) { w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w; };
+    fetch(0, blockIdx.x);
+    const float2 off = both(a.off);
     int turn = 0;
     for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
         const size_t at = static_cast<size_t>(m) * a.C;
-        uint32_t dn[S::W], r[S::W], y[S::W], ds[S::W];
-        S::load(dn, a.dn + at, a.C);
-        S::load(r, a.r + at, a.C);
-        if (a.dres) S::load(ds, a.dres + at, a.C);
-        if (a.y) S::load(y, a.y + at, a.C);
-        const float rr = a.rstd[a.M + m];
-        float s1 = 0.0f;
+        const bool more = m + gridDim.x < a.M;
+        if (more) fetch(turn ^ 1, m + gridDim.x);
+        const float2 rr = both(a.rstd[a.M + m]);
+        const float2 ry = both(post ? a.rstd[m] : 1.0f);
+        pipe.wait(more);
+        float2 s = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) {
-            if (S::col(e / VEC) >= a.C) continue;
-            const float xh = S::get(r, e) * rr, d = S::get(dn, e);
-            add(acc_pre, 0, e, d * xh);
-            s1 = fmaf(d * (S::get(wpre, e) + a.off), xh, s1);
+        for (int g = 0; g < G; ++g) {
+            uint32_t dn[4], r[4], w[4];
+            words(pipe.read(turn, 0, a.dn + at, g), dn);
+            words(pipe.read(turn, 1, a.r + at, g), r);
+            words(S::load(a.pre, g, a.C), w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 xh = fmul2(unpack_bf16x2(r[i]), rr), d = unpack_bf16x2(dn[i]);
+                add(acc_pre, 0, g, i, d, xh);
+                s = ffma2(fmul2(d, fadd2(unpack_bf16x2(w[i]), off)), xh, s);
+            }
         }
-        s1 = block_sum<T>(s1, buf[2 * turn]) * inv_c;
-        float dt[S::E];
+        // mean(dh xh) rstd, negated: d_r = rstd (dh - xh mean) is fma(xh, it, dh rstd)
+        const float2 c1 = both(-block_sum<T>(s, buf[turn][0]) * inv_c * rr.x);
+        float2 dt[G][4];
+        s = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) {
-            const float xh = S::get(r, e) * rr, dh = S::get(dn, e) * (S::get(wpre, e) + a.off);
-            float d = rr * (dh - xh * s1);
-            if (a.dres) d += S::get(ds, e);
-            S::put(r, e, to_bf16_bits(d));
-            dt[e] = a.alpha * d;
-        }
-        S::store(r, a.dx + at, a.C);
-        if (!a.y) continue;
-        uint32_t wpost[S::W];
-        const float ry = post ? a.rstd[m] : 1.0f;
-        if (post) S::load(wpost, a.post, a.C);
-        if (a.gate_kind != kGateNone) {
-            uint32_t g[S::W];
-            S::load(g, a.gate + (chan ? 0 : at), a.C);
-            uint32_t dg[S::W];
+        for (int g = 0; g < G; ++g) {
+            uint32_t dn[4], r[4], w[4], dx[4];
+            words(pipe.read(turn, 0, a.dn + at, g), dn);
+            words(pipe.read(turn, 1, a.r + at, g), r);
+            words(S::load(a.pre, g, a.C), w);
 #pragma unroll
-            for (int e = 0; e < S::E; ++e) {
-                float u = S::get(y, e);
-                if (post) u = u * ry * (S::get(wpost, e) + a.off);
-                if (chan) {
-                    if (S::col(e / VEC) < a.C) add(acc_gate, post ? 2 : 1, e, dt[e] * u);
-                } else {
-                    S::put(dg, e, to_bf16_bits(dt[e] * u));
+            for (int i = 0; i < 4; ++i) {
+                const float2 xh = fmul2(unpack_bf16x2(r[i]), rr);
+                const float2 dh = fmul2(unpack_bf16x2(dn[i]), fadd2(unpack_bf16x2(w[i]), off));
+                dt[g][i] = ffma2(xh, c1, fmul2(dh, rr));
+            }
+            if (a.dres) {
+                words(pipe.read(turn, dres_at, a.dres + at, g), w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dt[g][i] = fadd2(dt[g][i], unpack_bf16x2(w[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dx[i] = pack_bf16x2(dt[g][i]);
+            S::store(a.dx + at, g, a.C, dx);
+            if (!a.y) continue;
+            uint32_t y[4], p[4];
+            words(pipe.read(turn, y_at, a.y + at, g), y);
+            if (post) words(S::load(a.post, g, a.C), p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dt[g][i] = fmul2(dt[g][i], both(a.alpha));
+            if (chan || token) {
+                words(token ? pipe.read(turn, gate_at, a.gate + at, g) : S::load(a.gate, g, a.C), w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float2 u = unpack_bf16x2(y[i]);
+                    if (post) u = fmul2(fmul2(u, ry), fadd2(unpack_bf16x2(p[i]), off));
+                    if (chan) add(acc_gate, post ? 2 : 1, g, i, dt[g][i], u);
+                    else dx[i] = pack_bf16x2(fmul2(dt[g][i], u));
+                    dt[g][i] = fmul2(dt[g][i], unpack_bf16x2(w[i]));
                 }
-                dt[e] *= S::get(g, e);
+                if (token) S::store(a.dgate_token + at, g, a.C, dx);
             }
-            if (!chan) S::store(dg, a.dgate_token + at, a.C);
-        }
-        if (post) {
-            float s2 = 0.0f;
+            if (post) {
 #pragma unroll
-            for (int e = 0; e < S::E; ++e) {
-                if (S::col(e / VEC) >= a.C) continue;
-                const float yh = S::get(y, e) * ry;
-                add(acc_post, 1, e, dt[e] * yh);
-                dt[e] *= S::get(wpost, e) + a.off;
-                s2 = fmaf(dt[e], yh, s2);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 yh = fmul2(unpack_bf16x2(y[i]), ry);
+                    add(acc_post, 1, g, i, dt[g][i], yh);
+                    dt[g][i] = fmul2(dt[g][i], fadd2(unpack_bf16x2(p[i]), off));
+                    s = ffma2(dt[g][i], yh, s);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dx[i] = pack_bf16x2(dt[g][i]);
+                S::store(a.dy + at, g, a.C, dx);
             }
-            s2 = block_sum<T>(s2, buf[2 * turn + 1]) * inv_c;
-#pragma unroll
-            for (int e = 0; e < S::E; ++e) dt[e] = ry * (dt[e] - S::get(y, e) * ry * s2);
         }
+        if (!post) continue;
+        const float2 c2 = both(-block_sum<T>(s, buf[turn][1]) * inv_c * ry.x);
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) S::put(y, e, to_bf16_bits(dt[e]));
-        S::store(y, a.dy + at, a.C);
+        for (int g = 0; g < G; ++g) {
+            uint32_t y[4];
+            words(pipe.read(turn, y_at, a.y + at, g), y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[i] = pack_bf16x2(ffma2(fmul2(unpack_bf16x2(y[i]), ry), c2, fmul2(dt[g][i], ry)));
+            S::store(a.dy + at, g, a.C, y);
+        }
     }
     const size_t slab = static_cast<size_t>(gridDim.x) * a.C;
     float* p = a.part + static_cast<size_t>(blockIdx.x) * a.C;
 #pragma unroll
-    for (int e = 0; e < S::E; ++e) {
-        const int c = S::col(e / VEC) + e % VEC;
-        if (c < a.C) {
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 v[3];
             if constexpr (ACC_SMEM) {
-                p[c] = acc_smem[e * T + threadIdx.x];
-                if (post) p[slab + c] = acc_smem[(S::E + e) * T + threadIdx.x];
-                if (chan) p[(post ? 2 : 1) * slab + c] = acc_smem[((post ? 2 : 1) * S::E + e) * T + threadIdx.x];
+                for (int k = 0; k < sums; ++k) v[k] = acc_smem[((k * G + g) * 4 + i) * T + threadIdx.x];
             } else {
-                p[c] = acc_pre[e];
-                if (post) p[slab + c] = acc_post[e];
-                if (chan) p[(post ? 2 : 1) * slab + c] = acc_gate[e];
+                v[0] = acc_pre[g][i];
+                v[1] = post ? acc_post[g][i] : acc_gate[g][i];
+                v[2] = acc_gate[g][i];
             }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < sums) {
+                    const int c0 = S::col(g, 2 * i), c1 = S::col(g, 2 * i + 1);
+                    if (VEC == 8) {      // c0 < C says the whole group is inside
+                        if (c0 < a.C) *reinterpret_cast<float2*>(p + k * slab + c0) = v[k];
+                    } else {
+                        if (c0 < a.C) p[k * slab + c0] = v[k].x;
+                        if (c1 < a.C) p[k * slab + c1] = v[k].y;
+                    }
+                }
         }
-    }
 }
 
-// out_k[c] = bf16(sum over the G partial rows of slab k), in a fixed order:
-// warp w of a block takes rows w, w + 8, ... of 32 columns, then the warps'
-// sums are added in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int G, int C,
+// out_k[c] = bf16(sum over the rows of slab k of the blocks' partial sums), in
+// a fixed order: a block takes 32 columns, its warps 4 rows each at a time
+// (8 lanes x 4 columns a row) when rows are whole 16 bytes, else one; the
+// threads' sums are added in order.
+__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int rows, int C,
                                                           uint16_t* o0, uint16_t* o1, uint16_t* o2) {
-    __shared__ float s[8][32];
+    __shared__ float s[32][33];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    const float* p = part + static_cast<size_t>(blockIdx.y) * G * C;
-    float v = 0.0f;
-    if (c < C) {
+    const float* p = part + static_cast<size_t>(blockIdx.y) * rows * C;
+    const bool quads = (C & 3) == 0;
+    if (quads) {
+        const int c = blockIdx.x * 32 + (lane & 7) * 4, r0 = warp * 4 + (lane >> 3);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < C) {
 #pragma unroll 8
-        for (int g = warp; g < G; g += 8) v += p[static_cast<size_t>(g) * C + c];
+            for (int r = r0; r < rows; r += 32) {
+                const float4 u = *reinterpret_cast<const float4*>(p + static_cast<size_t>(r) * C + c);
+                v.x += u.x;
+                v.y += u.y;
+                v.z += u.z;
+                v.w += u.w;
+            }
+        }
+        float* d = &s[r0][(lane & 7) * 4];
+        d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+    } else {
+        const int c = blockIdx.x * 32 + lane;
+        float v = 0.0f;
+        if (c < C) {
+#pragma unroll 8
+            for (int r = warp; r < rows; r += 8) v += p[static_cast<size_t>(r) * C + c];
+        }
+        s[warp][lane] = v;
     }
-    s[warp][lane] = v;
     __syncthreads();
+    const int c = blockIdx.x * 32 + lane;
     if (warp == 0 && c < C) {
         float t = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) t += s[w][lane];
+        for (int w = 0; w < (quads ? 32 : 8); ++w) t += s[w][lane];
         uint16_t* o = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
         o[c] = to_bf16_bits(t);
     }

@@ -4,26 +4,41 @@
 
 namespace {
 
-template <int T, int V, int VEC>
+// Bytes of a two-stage row pipe.
+template <int T, int G, int VEC>
+size_t pipe_bytes(int arrays) {
+    return VEC == 8 ? static_cast<size_t>(2) * arrays * G * T * 16 : 0;
+}
+
+template <int T, int G, int VEC>
 struct NormLaunch {
-    static w4_status run(const w4::NormArgs& a, cudaStream_t st) {
-        if (a.scales) launch_pdl(w4::block_norm_kernel<T, V, VEC, true>, dim3(a.M), dim3(T), 0, st, a);
-        else launch_pdl(w4::block_norm_kernel<T, V, VEC, false>, dim3(a.M), dim3(T), 0, st, a);
+    static w4_status run(const w4::NormArgs& a, int sms, cudaStream_t st) {
+        const size_t smem = pipe_bytes<T, G, VEC>(1 + (a.y ? 1 : 0) + (a.gate_kind == w4::kGateToken ? 1 : 0));
+        const int grid = std::min(a.M, sms * (1024 / T));
+        auto fn = a.scales ? w4::block_norm_kernel<T, G, VEC, true> : w4::block_norm_kernel<T, G, VEC, false>;
+        if (smem > 40 * 1024 && ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
+        launch_pdl(fn, dim3(grid), dim3(T), smem, st, a);
         return launch_status();
     }
 };
 
-// Blocks of the backward pass: two per SM (each leaves a partial row of the
-// weight gradients), one of 1024 threads.
-int norm_grad_blocks(int M, int C, int sms) { return std::min(M, C > 8192 ? sms : 2 * sms); }
+// Blocks of the backward pass; each leaves a partial row of the weights' gradients.
+template <int T, int G, int VEC>
+struct NormGradBlocks {
+    static int run(int M, int sms) {
+        return std::min(M, sms * w4::norm_grad_blocks_per_sm(T, G));
+    }
+};
+int norm_grad_blocks(int M, int C, int sms) { return dispatch_row<NormGradBlocks>(C, M, sms); }
 
-template <int T, int V, int VEC>
+template <int T, int G, int VEC>
 struct NormGradLaunch {
     static w4_status run(const w4::NormGradArgs& a, int blocks, int sums, cudaStream_t st) {
         constexpr bool kSmem = T == 1024;
-        const size_t smem = kSmem ? static_cast<size_t>(sums) * T * V * VEC * sizeof(float) : 0;
-        auto fn = w4::block_norm_backward_kernel<T, V, VEC, kSmem>;
-        if (smem > 48 * 1024 && ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
+        const int arrays = 2 + (a.dres ? 1 : 0) + (a.y ? 1 : 0) + (a.gate_kind == w4::kGateToken ? 1 : 0);
+        const size_t smem = kSmem ? static_cast<size_t>(sums) * T * G * 8 * sizeof(float) : pipe_bytes<T, G, VEC>(arrays);
+        auto fn = w4::block_norm_backward_kernel<T, G, VEC, kSmem>;
+        if (smem > 40 * 1024 && ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
         launch_pdl(fn, dim3(blocks), dim3(T), smem, st, a);
         return launch_status();
     }
@@ -69,7 +84,7 @@ w4_status w4_block_norm(const void* x, const void* y, int M, int C, const void* 
     a.alpha = residual_scale;
     a.off = weight_offset;
     a.eps = eps;
-    return dispatch_row<NormLaunch>(C, a, static_cast<cudaStream_t>(stream));
+    return dispatch_row<NormLaunch>(C, a, device_info(current_device()).sms, static_cast<cudaStream_t>(stream));
 }
 
 size_t w4_block_norm_workspace_bytes(int M, int C) {

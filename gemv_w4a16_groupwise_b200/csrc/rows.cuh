@@ -1,72 +1,110 @@
-// Rows of bf16 held in the registers of a thread block, and reductions over
-// the block.
+// Rows of bf16 worked on by a thread block, and reductions over the block.
 #pragma once
 
 #include "common.cuh"
 
 namespace w4 {
 
-constexpr int kRowMaxC = 16384;   // 1024 threads x 2 vectors of 8
+constexpr int kRowMaxC = 16384;   // 1024 threads x 2 groups of 8
 
-// Elements of one thread: V vectors of VEC consecutive columns, T vectors
-// apart.  VEC = 8 needs C % 8 == 0 (16-byte aligned rows); VEC = 1 serves
-// the other widths.
-template <int T, int V, int VEC>
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void cp_async_16_zfill(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ float2 unpack_bf16x2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float2 v) { return bf162_bits(__floats2bfloat162_rn(v.x, v.y)); }
+__device__ __forceinline__ uint16_t to_bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A thread's columns of a row: G groups of 8 values, held as 4 words of
+// bf16x2.  VEC = 8: a group is 8 consecutive columns, groups of the block's
+// threads side by side (rows of whole 16 bytes).  VEC = 1: its values lie T
+// columns apart, for the other widths.  Columns past C read as 0, which is
+// neutral in every sum and maximum here.
+template <int T, int G, int VEC>
 struct RowSpan {
-    static constexpr int E = V * VEC;                       // elements of a thread
-    static constexpr int W = VEC == 8 ? V * 4 : (V + 1) / 2;   // packed words
-    __device__ static __forceinline__ int col(int j) {      // first column of vector j
-        return (j * T + static_cast<int>(threadIdx.x)) * VEC;
+    __device__ static __forceinline__ int col(int g, int i) {     // column of value i of group g
+        return VEC == 8 ? (g * T + static_cast<int>(threadIdx.x)) * 8 + i
+                        : (g * 8 + i) * T + static_cast<int>(threadIdx.x);
     }
-    __device__ static __forceinline__ float get(const uint32_t (&p)[W], int e) {
-        return __uint_as_float((e & 1) ? (p[e >> 1] & 0xFFFF0000u) : (p[e >> 1] << 16));
-    }
-    __device__ static __forceinline__ void put(uint32_t (&p)[W], int e, uint16_t b) {
-        if (e & 1) p[e >> 1] = (p[e >> 1] & 0xFFFFu) | (static_cast<uint32_t>(b) << 16);
-        else p[e >> 1] = (p[e >> 1] & 0xFFFF0000u) | b;
-    }
-    __device__ static __forceinline__ void load(uint32_t (&p)[W], const uint16_t* row, int C) {
+    __device__ static __forceinline__ uint4 load(const uint16_t* row, int g, int C) {
+        if constexpr (VEC == 8) {
+            const int c = col(g, 0);
+            return c < C ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < W; ++i) p[i] = 0u;              // columns past C read as 0
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = col(j);
-            if (c < C) {
-                if constexpr (VEC == 8) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(row + c);
-                    p[4 * j] = v.x;
-                    p[4 * j + 1] = v.y;
-                    p[4 * j + 2] = v.z;
-                    p[4 * j + 3] = v.w;
-                } else {
-                    put(p, j, row[c]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int c0 = col(g, 2 * i), c1 = col(g, 2 * i + 1);
+                w[i] = (c0 < C ? row[c0] : 0u) | ((c1 < C ? static_cast<uint32_t>(row[c1]) : 0u) << 16);
             }
+            return make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    __device__ static __forceinline__ void store(const uint32_t (&p)[W], uint16_t* row, int C) {
+    __device__ static __forceinline__ void store(uint16_t* row, int g, int C, const uint32_t (&w)[4]) {
+        if constexpr (VEC == 8) {
+            const int c = col(g, 0);
+            if (c < C) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = col(j);
-            if (c < C) {
-                if constexpr (VEC == 8)
-                    *reinterpret_cast<uint4*>(row + c) = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-                else
-                    row[c] = static_cast<uint16_t>((j & 1) ? p[j >> 1] >> 16 : p[j >> 1] & 0xFFFFu);
+            for (int i = 0; i < 4; ++i) {
+                const int c0 = col(g, 2 * i), c1 = col(g, 2 * i + 1);
+                if (c0 < C) row[c0] = static_cast<uint16_t>(w[i]);
+                if (c1 < C) row[c1] = static_cast<uint16_t>(w[i] >> 16);
             }
         }
     }
 };
 
-__device__ __forceinline__ uint16_t to_bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+// Rows on their way from device memory: every thread copies its own groups of
+// the next row ahead (cp.async) and later reads back what it copied itself, so
+// the pipe needs no barriers, and no registers for what is in flight or must
+// be read again after a reduction.  Two stages of `arrays` rows; without the
+// pipe (PIPED = false) a read goes to memory.
+template <int T, int G, int VEC, bool PIPED>
+struct RowPipe {
+    using S = RowSpan<T, G, VEC>;
+    uint4* base;             // [2][arrays][G * T]
+    int arrays, C;
+    __device__ __forceinline__ void fetch(int stage, int array, const uint16_t* row) const {
+        if constexpr (PIPED) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int c = S::col(g, 0);
+                cp_async_16_zfill(base + (stage * arrays + array) * (G * T) + g * T + threadIdx.x,
+                                  row + (c < C ? c : 0), c < C);
+            }
+        }
+    }
+    __device__ __forceinline__ void commit() const {
+        if constexpr (PIPED) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // all but the newest `newer` (0 or 1) groups have landed
+    __device__ __forceinline__ void wait(bool newer) const {
+        if constexpr (PIPED) {
+            if (newer) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ uint4 read(int stage, int array, const uint16_t* row, int g) const {
+        if constexpr (PIPED) return base[(stage * arrays + array) * (G * T) + g * T + threadIdx.x];
+        else return S::load(row, g, C);
+    }
+};
 
-// Sum over the block's T threads in a fixed order, in every thread.  `buf`
-// alternates between calls, so that one barrier per call is enough.
+// Sum over the block's T threads in a fixed order, in every thread.  One
+// barrier; `buf` is not written again before another barrier has passed.
 template <int T>
-__device__ __forceinline__ float block_sum(float v, float* buf) {
+__device__ __forceinline__ float block_sum(float2 v2, float* buf) {
+    float v = v2.x + v2.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if constexpr (T == 32) return v;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.0f;
@@ -75,12 +113,11 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
     return s;
 }
 
-// Maximum of the bit patterns over the block (order-independent; as bits, a
-// NaN is larger than an infinity and neither is dropped).
+// Maximum of non-negative values as bit patterns (order-independent; a NaN is
+// larger than an infinity and neither is dropped).
 template <int T>
 __device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* buf) {
     v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if constexpr (T == 32) return v;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
     uint32_t t = 0;
@@ -88,5 +125,15 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* buf) {
     for (int w = 0; w < T / 32; ++w) t = max(t, buf[w]);
     return t;
 }
+
+// max(m, |v.x|, |v.y|), a NaN kept (the three-operand form of sm_100)
+__device__ __forceinline__ float max_abs(float m, float2 v) {
+    asm("{\n .reg .f32 a, b;\n abs.f32 a, %1;\n abs.f32 b, %2;\n max.NaN.f32 %0, %0, a, b;\n}\n"
+        : "+f"(m)
+        : "f"(v.x), "f"(v.y));
+    return m;
+}
+// the larger magnitudes of two pairs of bf16, as bits
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
 
 }  // namespace w4

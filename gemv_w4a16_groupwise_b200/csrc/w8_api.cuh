@@ -14,29 +14,24 @@ w4_status check_w8(int M, int N, int K, long long ldw, int transposed, const voi
     return W4_OK;
 }
 
-// The block of a row of C: the fewest threads that hold it in one vector of
-// 8 each, up to 512, then two vectors each.
+// The block of a row of C: threads T and groups of 8 values each.  One group
+// as far as 2048; two from there, with half the threads.
 template <template <int, int, int> class Launch, typename... Args>
-w4_status dispatch_row(int C, Args... args) {
+auto dispatch_row(int C, Args... args) {
     const bool vec = C % 8 == 0;
-    if (C <= 1024) return vec ? Launch<128, 1, 8>::run(args...) : Launch<128, 8, 1>::run(args...);
-    if (C <= 2048) return vec ? Launch<256, 1, 8>::run(args...) : Launch<256, 8, 1>::run(args...);
-    if (C <= 4096) return vec ? Launch<256, 2, 8>::run(args...) : Launch<256, 16, 1>::run(args...);
-    if (C <= 8192) return vec ? Launch<512, 2, 8>::run(args...) : Launch<512, 16, 1>::run(args...);
-    return vec ? Launch<1024, 2, 8>::run(args...) : Launch<1024, 16, 1>::run(args...);
+    if (C <= 1024) return vec ? Launch<128, 1, 8>::run(args...) : Launch<128, 1, 1>::run(args...);
+    if (C <= 2048) return vec ? Launch<256, 1, 8>::run(args...) : Launch<256, 1, 1>::run(args...);
+    if (C <= 4096) return vec ? Launch<256, 2, 8>::run(args...) : Launch<256, 2, 1>::run(args...);
+    if (C <= 8192) return vec ? Launch<512, 2, 8>::run(args...) : Launch<512, 2, 1>::run(args...);
+    return vec ? Launch<1024, 2, 8>::run(args...) : Launch<1024, 2, 1>::run(args...);
 }
 
-template <int T, int V, int VEC>
+template <int T, int G, int VEC>
 struct QuantizeLaunch {
     static w4_status run(const uint16_t* X, int R, int C, const float* channel, int8_t* codes, long long ld,
                          float* scales, int sms, cudaStream_t st) {
-        const int grid = std::min(R, sms * (2048 / T));     // what the SMs hold at once
-        if (channel)
-            launch_pdl(w4::quantize_rows_kernel<T, V, VEC, true>, dim3(grid), dim3(T), 0, st, X, R, C, channel, codes,
-                       ld, scales);
-        else
-            launch_pdl(w4::quantize_rows_kernel<T, V, VEC, false>, dim3(grid), dim3(T), 0, st, X, R, C, channel, codes,
-                       ld, scales);
+        auto fn = channel ? w4::quantize_rows_kernel<T, G, VEC, true> : w4::quantize_rows_kernel<T, G, VEC, false>;
+        launch_pdl(fn, dim3(std::min(R, sms * (1024 / T))), dim3(T), 0, st, X, R, C, channel, codes, ld, scales);
         return launch_status();
     }
 };

@@ -49,14 +49,6 @@ __device__ __forceinline__ uint4 ldg_stream_16(const void* p) {
     return v;
 }
 
-// 16 bytes to shared memory, or zeros.
-__device__ __forceinline__ void cp_async_16_zfill(void* dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                 "l"(src), "r"(in ? 16 : 0)
-                 : "memory");
-}
-
 // Bytes k .. k + 15 of a row of K, zero from K on.
 __device__ __forceinline__ uint4 mask_tail(uint4 v, int k, int K) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -120,10 +112,9 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             const uint4 x = raw[v * kGvWarps * 32 + threadIdx.x];
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max((u[i] & 0x7FFFu) << 16, u[i] & 0x7FFF0000u));
+            top = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(top, x.x), x.y), x.z), x.w);
         }
+        top = max(top << 16, top & 0xFFFF0000u);
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         if (lane == 0) tops[warp] = top;
         __syncthreads();
@@ -138,10 +129,7 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
             const int k = (v * kT + i0) * 8;
             if (k < tb - 64) {
                 const uint4 x = raw[v * kGvWarps * 32 + threadIdx.x];
-                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = __uint_as_float((i & 1) ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+                float2 f[4] = {unpack_bf16x2(x.x), unpack_bf16x2(x.y), unpack_bf16x2(x.z), unpack_bf16x2(x.w)};
                 *reinterpret_cast<uint2*>(tokens + m * tb + k) = codes8(f, sc);
             }
         }

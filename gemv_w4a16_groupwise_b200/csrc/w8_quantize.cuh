@@ -20,12 +20,10 @@
 
 namespace w4 {
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
 struct RowScale {
     float scale;   // value of one code
     float inv;     // codes per unit of v pre
-    float pre;     // a power of two that keeps inv finite for tiny rows
+    float pre;     // 1, a power of two that keeps inv finite for tiny rows, or 0 for a poisoned row
 };
 
 __device__ __forceinline__ RowScale row_scale(float top) {
@@ -37,138 +35,152 @@ __device__ __forceinline__ RowScale row_scale(float top) {
         return s;
     }
     s.scale = __fdiv_rn(top, 127.0f);
-    s.pre = top < 1.2676506e-30f ? 18446744073709551616.0f : 1.0f;      // below 2^-99: times 2^64
+    s.pre = top < 1.5777218e-30f ? 18446744073709551616.0f : 1.0f;      // below 2^-99: times 2^64
     s.inv = top > 0.0f ? __fdiv_ru(127.0f, top * s.pre) : 0.0f;
     return s;
 }
 
-// rint(v inv) in the low byte: adding 1.5 * 2^23 leaves the integer, rounded
-// half to even, in the low mantissa bits.  A poisoned row (pre = 0) gives 0:
-// its values are replaced before the product, as 0 times an infinity is not 0.
-__device__ __forceinline__ uint32_t code_bits(float v, const RowScale& s) {
-    const float u = s.pre == 1.0f ? v : (s.pre == 0.0f ? 0.0f : v * s.pre);
-    return __float_as_uint(fmaf(u, s.inv, 12582912.0f));
-}
-__device__ __forceinline__ int8_t code1(float v, const RowScale& s) {
-    return static_cast<int8_t>(code_bits(v, s) & 0xFFu);
-}
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const RowScale& s) {
-    const uint32_t lo = prmt(code_bits(a, s), code_bits(b, s), 0x0040u);
-    const uint32_t hi = prmt(code_bits(c, s), code_bits(d, s), 0x0040u);
-    return prmt(lo, hi, 0x5410u);
-}
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], const RowScale& s) {
-    return make_uint2(codes4(v[0], v[1], v[2], v[3], s), codes4(v[4], v[5], v[6], v[7], s));
+// Eight values as codes: rint(v inv) is in the low byte after adding
+// 1.5 * 2^23, which leaves the integer, rounded half to even, in the low
+// mantissa bits.
+__device__ __forceinline__ uint2 codes8(float2 (&v)[4], const RowScale& s) {
+    if (s.pre != 1.0f) {       // the whole row: tiny, or poisoned (0 times an infinity is not 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = s.pre == 0.0f ? both(0.0f) : fmul2(v[i], both(s.pre));
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = ffma2(v[i], both(s.inv), both(12582912.0f));
+        w[i] = prmt(__float_as_uint(f.x), __float_as_uint(f.y), 0x0040u);
+    }
+    return make_uint2(prmt(w[0], w[1], 0x5410u), prmt(w[2], w[3], 0x5410u));
 }
 
-// The channel factors of a thread's columns, kept over its rows.
-template <int T, int V, int VEC>
-struct ChannelSpan {
-    using S = RowSpan<T, V, VEC>;
-    float f[S::E];
-    __device__ __forceinline__ void load(const float* channel, int C) {
+// The codes of a thread's group to its row.
+template <class S, int VEC>
+__device__ __forceinline__ void store_codes(int8_t* row, int g, int C, uint2 w) {
+    if constexpr (VEC == 8) {
+        const int c = S::col(g, 0);
+        if (c < C) *reinterpret_cast<uint2*>(row + c) = w;
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = S::col(j);
-            if constexpr (VEC == 8) {
-                const bool in = c < C;
-                const float4 lo = in ? *reinterpret_cast<const float4*>(channel + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-                const float4 hi = in ? *reinterpret_cast<const float4*>(channel + c + 4) : lo;
-                f[8 * j] = lo.x, f[8 * j + 1] = lo.y, f[8 * j + 2] = lo.z, f[8 * j + 3] = lo.w;
-                f[8 * j + 4] = hi.x, f[8 * j + 5] = hi.y, f[8 * j + 6] = hi.z, f[8 * j + 7] = hi.w;
-            } else {
-                f[j] = c < C ? channel[c] : 0.0f;
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int c = S::col(g, i);
+            if (c < C) row[c] = static_cast<int8_t>((i < 4 ? w.x >> (8 * i) : w.y >> (8 * (i - 4))) & 0xFFu);
         }
     }
-};
+}
+
+// A group's values times their channel factors.
+template <class S, int VEC>
+__device__ __forceinline__ void channel_values(float2 (&v)[4], uint4 x, const float* __restrict__ channel, int g,
+                                               int C) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = unpack_bf16x2(w[i]);
+    if (channel == nullptr) return;
+    if constexpr (VEC == 8) {
+        const int c = S::col(g, 0);
+        if (c < C) {
+            const float4 lo = __ldg(reinterpret_cast<const float4*>(channel + c));
+            const float4 hi = __ldg(reinterpret_cast<const float4*>(channel + c + 4));
+            v[0] = fmul2(v[0], make_float2(lo.x, lo.y));
+            v[1] = fmul2(v[1], make_float2(lo.z, lo.w));
+            v[2] = fmul2(v[2], make_float2(hi.x, hi.y));
+            v[3] = fmul2(v[3], make_float2(hi.z, hi.w));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c0 = S::col(g, 2 * i), c1 = S::col(g, 2 * i + 1);
+            v[i] = fmul2(v[i], make_float2(c0 < C ? __ldg(channel + c0) : 0.0f, c1 < C ? __ldg(channel + c1) : 0.0f));
+        }
+    }
+}
 
 // Rows of at most 16384: a block holds a row in registers between the maximum
-// and the codes, so the row is read once.  Bound by device memory (3 bytes an
-// element).  Blocks walk over the rows and keep the channel factors, which
-// would otherwise be twice a row's own bytes from L2 every time.
-template <int T, int V, int VEC, bool CHANNEL>
-__global__ void __launch_bounds__(T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
-                                                          const float* __restrict__ channel,
-                                                          int8_t* __restrict__ codes, long long ld,
-                                                          float* __restrict__ scales) {
-    using S = RowSpan<T, V, VEC>;
+// and the codes, so the row is read once, and has the next row's loads under
+// way meanwhile.  Bound by device memory (3 bytes an element).  The channel
+// factors (twice a row's bytes) come from L1 every time.
+template <int T, int G, int VEC, bool CHANNEL>
+__global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
+                                                                    const float* __restrict__ channel,
+                                                                    int8_t* __restrict__ codes, long long ld,
+                                                                    float* __restrict__ scales) {
+    using S = RowSpan<T, G, VEC>;
     __shared__ uint32_t buf[2][32];
     pdl_wait();
     pdl_launch_dependents();
-    ChannelSpan<T, V, VEC> ch;
-    if constexpr (CHANNEL) ch.load(channel, C);
+    uint4 x[G], next[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) next[g] = S::load(X + static_cast<size_t>(blockIdx.x) * C, g, C);
     int turn = 0;
     for (long long m = blockIdx.x; m < R; m += gridDim.x, turn ^= 1) {
-        uint32_t p[S::W];
-        S::load(p, X + static_cast<size_t>(m) * C, C);
-        auto value = [&](int e) { return CHANNEL ? S::get(p, e) * ch.f[e] : S::get(p, e); };
-        uint32_t top = 0;       // columns past C read as 0
+        const bool more = m + gridDim.x < R;
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) top = max(top, abs_bits(value(e)));
+        for (int g = 0; g < G; ++g) {
+            x[g] = next[g];
+            if (more) next[g] = S::load(X + static_cast<size_t>(m + gridDim.x) * C, g, C);
+        }
+        uint32_t top;
+        if constexpr (CHANNEL) {
+            float t = 0.0f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float2 v[4];
+                channel_values<S, VEC>(v, x[g], channel, g, C);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t = max_abs(t, v[i]);
+            }
+            top = __float_as_uint(t);
+        } else {
+            uint32_t t = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                t = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(t, x[g].x), x[g].y), x[g].z), x[g].w);
+            top = max(t << 16, t & 0xFFFF0000u);
+        }
         top = block_max_bits<T>(top, buf[turn]);
         const RowScale sc = row_scale(__uint_as_float(top));
         if (threadIdx.x == 0) scales[m] = sc.scale;
-        int8_t* q = codes + static_cast<size_t>(m) * ld;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = S::col(j);
-            if (c < C) {
-                if constexpr (VEC == 8) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = value(8 * j + i);
-                    *reinterpret_cast<uint2*>(q + c) = codes8(v, sc);
-                } else {
-                    q[c] = code1(value(j), sc);
-                }
-            }
+        for (int g = 0; g < G; ++g) {
+            float2 v[4];
+            channel_values<S, VEC>(v, x[g], CHANNEL ? channel : nullptr, g, C);
+            store_codes<S, VEC>(codes + static_cast<size_t>(m) * ld, g, C, codes8(v, sc));
         }
     }
 }
 
-// Longer rows: the second pass reads the row again (from L2).
+// Longer rows: a block takes a row 8192 values at a time, and the second pass
+// reads it again (from L2).
 template <int VEC>
 __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t* __restrict__ X, int C,
                                                                   const float* __restrict__ channel,
                                                                   int8_t* __restrict__ codes, long long ld,
                                                                   float* __restrict__ scales) {
+    using S = RowSpan<1024, 1, VEC>;
     __shared__ uint32_t buf[32];
     const size_t m = blockIdx.x;
     const uint16_t* x = X + m * C;
     pdl_wait();
     pdl_launch_dependents();
-    auto load = [&](int c, float (&v)[VEC]) {
-        if constexpr (VEC == 8) {
-            const uint4 w = *reinterpret_cast<const uint4*>(x + c);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((i & 1) ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
-        } else {
-            v[0] = bf16_bits_to_float(x[c]);
-        }
-        if (channel) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] *= channel[c + i];
-        }
-    };
-    uint32_t top = 0;
+    float t = 0.0f;
 #pragma unroll 2
-    for (int c = threadIdx.x * VEC; c < C; c += 1024 * VEC) {
-        float v[VEC];
-        load(c, v);
+    for (int c = 0; c < C; c += 8192) {
+        float2 v[4];
+        channel_values<S, VEC>(v, S::load(x + c, 0, C - c), channel ? channel + c : nullptr, 0, C - c);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) top = max(top, abs_bits(v[i]));
+        for (int i = 0; i < 4; ++i) t = max_abs(t, v[i]);
     }
-    const RowScale sc = row_scale(__uint_as_float(block_max_bits<1024>(top, buf)));
+    const RowScale sc = row_scale(__uint_as_float(block_max_bits<1024>(__float_as_uint(t), buf)));
     if (threadIdx.x == 0) scales[m] = sc.scale;
-    int8_t* q = codes + m * ld;
 #pragma unroll 2
-    for (int c = threadIdx.x * VEC; c < C; c += 1024 * VEC) {
-        float v[VEC];
-        load(c, v);
-        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q + c) = codes8(v, sc);
-        else q[c] = code1(v[0], sc);
+    for (int c = 0; c < C; c += 8192) {
+        float2 v[4];
+        channel_values<S, VEC>(v, S::load(x + c, 0, C - c), channel ? channel + c : nullptr, 0, C - c);
+        store_codes<S, VEC>(codes + m * ld + c, 0, C - c, codes8(v, sc));
     }
 }
 
