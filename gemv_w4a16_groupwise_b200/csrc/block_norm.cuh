@@ -45,13 +45,14 @@ struct NormArgs {
 // A block walks over rows blockIdx.x, + gridDim.x, ... with the next row's
 // loads under way while it works on one.  The values are worked on in pairs
 // (f32x2): with scalar arithmetic and predicated sums the kernel was bound by
-// the instructions it issued, not by memory.
+// the instructions it issued, not by memory.  rsqrtf is within 2 ulp, less than
+// the sum under it is.
 template <int T, int G, int VEC, bool CODES>
 __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs a) {
     using S = RowSpan<T, G, VEC>;
     extern __shared__ uint4 ring[];
-    __shared__ float buf[2][2][32];      // [row's parity][reduction]
-    __shared__ uint32_t ubuf[2][32];
+    __shared__ __align__(16) float buf[2][2][32];      // [row's parity][reduction]
+    __shared__ __align__(16) uint32_t ubuf[2][32];
     const float inv_c = 1.0f / static_cast<float>(a.C);
     const bool post = a.post != nullptr, token = a.gate_kind == kGateToken, gated = a.gate_kind != kGateNone;
     const RowPipe<T, G, VEC, VEC == 8> pipe = {ring, 1 + (a.y ? 1 : 0) + (token ? 1 : 0), a.C};
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
                     ss = ffma2(v, v, ss);
                 }
             }
-            rstd_y = 1.0f / sqrtf(block_sum<T>(ss, buf[turn][0]) * inv_c + a.eps);
+            rstd_y = rsqrtf(block_sum<T>(ss, buf[turn][0]) * inv_c + a.eps);
         }
         uint32_t r[G][4];
         float2 ss = both(0.0f);
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
                 ss = ffma2(v, v, ss);
             }
         }
-        const float rstd = 1.0f / sqrtf(block_sum<T>(ss, buf[turn][1]) * inv_c + a.eps);
+        const float rstd = rsqrtf(block_sum<T>(ss, buf[turn][1]) * inv_c + a.eps);
         if (a.rstd && threadIdx.x == 0) {
             a.rstd[m] = rstd_y;
             a.rstd[a.M + m] = rstd;
@@ -139,8 +140,9 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
             if constexpr (!CODES) S::store(static_cast<uint16_t*>(a.normed) + at, g, a.C, r[g]);
         }
         if constexpr (CODES) {
-            const RowScale sc = row_scale(__uint_as_float(block_max_bits<T>(__float_as_uint(top), ubuf[turn])));
-            if (threadIdx.x == 0) a.scales[m] = sc.scale;
+            top = __uint_as_float(block_max_bits<T>(__float_as_uint(top), ubuf[turn]));
+            const RowCodes sc = row_codes(top);
+            if (threadIdx.x == 0) a.scales[m] = row_scale(top);
 #pragma unroll
             for (int g = 0; g < G; ++g)
                 store_codes<S, VEC>(static_cast<int8_t*>(a.normed) + static_cast<size_t>(m) * a.ld, g, a.C,
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
     constexpr int kRegs = ACC_SMEM ? 1 : G;
     extern __shared__ uint4 dyn_smem[];     // the row pipe; with ACC_SMEM the sums, [sums][G][4][T]
     float2* acc_smem = reinterpret_cast<float2*>(dyn_smem);
-    __shared__ float buf[2][2][32];
+    __shared__ __align__(16) float buf[2][2][32];
     const float inv_c = 1.0f / static_cast<float>(a.C);
     const bool post = a.post != nullptr, chan = a.gate_kind == kGateChannel, token = a.gate_kind == kGateToken;
     pdl_launch_dependents();

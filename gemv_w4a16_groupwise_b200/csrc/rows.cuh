@@ -99,7 +99,7 @@ struct RowPipe {
 };
 
 // Sum over the block's T threads in a fixed order, in every thread.  One
-// barrier; `buf` is not written again before another barrier has passed.
+// barrier; `buf` (32 entries, 16-byte aligned) is not written again before another barrier has passed.
 template <int T>
 __device__ __forceinline__ float block_sum(float2 v2, float* buf) {
     float v = v2.x + v2.y;
@@ -109,7 +109,10 @@ __device__ __forceinline__ float block_sum(float2 v2, float* buf) {
     __syncthreads();
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) s += buf[w];
+    for (int w = 0; w < T / 32; w += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(buf + w);
+        s += (u.x + u.y) + (u.z + u.w);
+    }
     return s;
 }
 
@@ -122,7 +125,10 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* buf) {
     __syncthreads();
     uint32_t t = 0;
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) t = max(t, buf[w]);
+    for (int w = 0; w < T / 32; w += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(buf + w);
+        t = max(t, max(max(u.x, u.y), max(u.z, u.w)));
+    }
     return t;
 }
 

@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
         top = 0;
 #pragma unroll
         for (int w = 0; w < kT / 32; ++w) top = max(top, tops[m * (kT / 32) + w]);
-        const RowScale sc = row_scale(__uint_as_float(top));
-        if (i0 == 0) token_scale[m] = sc.scale;
+        const RowCodes sc = row_codes(__uint_as_float(top));
+        if (i0 == 0) token_scale[m] = row_scale(__uint_as_float(top));
         // codes, and zeros up to the end of the block's last step
 #pragma unroll
         for (int v = 0; v < kV; ++v) {

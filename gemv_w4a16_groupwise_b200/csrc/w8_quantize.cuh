@@ -4,47 +4,65 @@
 // with an infinity or a NaN has s = NaN and q = 0, so all it takes part in is
 // NaN.
 //
-// The quotient is not divided out per element: with inv = 127 / max |v|
-// rounded up, the code is rint(v inv), one fma.  For bf16 v this is the exact
-// quotient rounded half to even.  Write v = i 2^-d and max |v| = b in units of
-// the maximum's last place, b in [128, 255], |i| <= 255: the quotient is
-// 127 i 2^-d / b, and its distance from a rounding border h + 1/2 is a
-// multiple of 1 / (2^(d+1) b), at least 2^-(d+9) when not zero, against an
-// error of at most |q| 2^-23 < 2^(8-d) 2^-23 from inv.  Ties: 254 i = (2h+1) b
-// 2^d needs 127 to divide b or 2h + 1; b = 254 makes inv a power of two, exact;
-// 2h + 1 = 127 is |q| = 63.5, which goes to 64, the even code and the side
-// that inv, rounded up, leans to.
+// The quotient is not divided out per element: the code is rint(v inv), one
+// fma, with inv at least 127 / max |v| and above it by less than 2^-21 of it.
+// For bf16 v this is the exact quotient rounded half to even.  Write
+// v = i 2^-d and max |v| = b in units of the maximum's last place, b in
+// [128, 255], |i| <= 255: the quotient is 127 i 2^-d / b, and its distance from
+// a rounding border h + 1/2 is a multiple of 1 / (2^(d+1) b), at least 2^-(d+9)
+// when not zero, against less than 2^(8-d) 2^-21 from inv.  Ties: 254 i =
+// (2h+1) b 2^d needs 127 to divide b or 2h + 1.  2h + 1 = 127 is |q| = 63.5,
+// which goes to 64, the even code and the side that inv leans to; b = 254 makes
+// 127 / max |v| a power of two, and inv is set to it exactly.
+//
+// inv is a reciprocal of the hardware's (within 2^-23) and a product: an IEEE
+// division in every thread of a row's block, and the scale's, cost more issue
+// slots than the row's own values.
 #pragma once
 
 #include "rows.cuh"
 
 namespace w4 {
 
-struct RowScale {
-    float scale;   // value of one code
+// What turns a row's values into codes.
+struct RowCodes {
     float inv;     // codes per unit of v pre
-    float pre;     // 1, a power of two that keeps inv finite for tiny rows, or 0 for a poisoned row
+    float pre;     // 1, a power of two that keeps inv normal for extreme rows, or 0 for a poisoned row
 };
 
-__device__ __forceinline__ RowScale row_scale(float top) {
-    RowScale s;
-    if (!(top < __uint_as_float(0x7F800000u))) {   // infinity or NaN
-        s.scale = __uint_as_float(0x7FC00000u);
-        s.inv = 0.0f;
-        s.pre = 0.0f;
+__device__ __forceinline__ RowCodes row_codes(float top) {
+    RowCodes s;
+    s.pre = 1.0f;
+    if (!(top < __uint_as_float(0x7F800000u))) {       // infinity or NaN
+        s.inv = s.pre = 0.0f;
         return s;
     }
-    s.scale = __fdiv_rn(top, 127.0f);
-    s.pre = top < 1.5777218e-30f ? 18446744073709551616.0f : 1.0f;      // below 2^-99: times 2^64
-    s.inv = top > 0.0f ? __fdiv_ru(127.0f, top * s.pre) : 0.0f;
+    // below 2^-99 or from 2^100 on the row is taken times 2^64 or 2^-64, so that
+    // the reciprocal stays a normal number
+    if (top < 1.5777218e-30f) s.pre = 18446744073709551616.0f;
+    if (top >= 1.2676506e30f) s.pre = 5.4210109e-20f;
+    top *= s.pre;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(top));
+    // 127 (1 + 2^-22), one ulp up: above the two roundings' 2^-23 + 2^-24
+    s.inv = r * 127.0000381f;
+    const uint32_t bits = __float_as_uint(top);
+    // 1.984375 2^e = 127 2^(e-6): the quotient is 2^(6-e)
+    if ((bits & 0x007FFFFFu) == 0x007E0000u) s.inv = __uint_as_float((260u - (bits >> 23)) << 23);
+    if (!(top > 0.0f)) s.inv = 0.0f;
     return s;
+}
+
+// A row's scale, the value of one code.
+__device__ __forceinline__ float row_scale(float top) {
+    return top < __uint_as_float(0x7F800000u) ? __fdiv_rn(top, 127.0f) : __uint_as_float(0x7FC00000u);
 }
 
 // Eight values as codes: rint(v inv) is in the low byte after adding
 // 1.5 * 2^23, which leaves the integer, rounded half to even, in the low
 // mantissa bits.
-__device__ __forceinline__ uint2 codes8(float2 (&v)[4], const RowScale& s) {
-    if (s.pre != 1.0f) {       // the whole row: tiny, or poisoned (0 times an infinity is not 0)
+__device__ __forceinline__ uint2 codes8(float2 (&v)[4], const RowCodes& s) {
+    if (s.pre != 1.0f) {       // the whole row: extreme, or poisoned (0 times an infinity is not 0)
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = s.pre == 0.0f ? both(0.0f) : fmul2(v[i], both(s.pre));
     }
@@ -109,7 +127,7 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
                                                                     int8_t* __restrict__ codes, long long ld,
                                                                     float* __restrict__ scales) {
     using S = RowSpan<T, G, VEC>;
-    __shared__ uint32_t buf[2][32];
+    __shared__ __align__(16) uint32_t buf[2][32];
     pdl_wait();
     pdl_launch_dependents();
     uint4 x[G], next[G];
@@ -142,8 +160,8 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
             top = max(t << 16, t & 0xFFFF0000u);
         }
         top = block_max_bits<T>(top, buf[turn]);
-        const RowScale sc = row_scale(__uint_as_float(top));
-        if (threadIdx.x == 0) scales[m] = sc.scale;
+        const RowCodes sc = row_codes(__uint_as_float(top));
+        if (threadIdx.x == 0) scales[m] = row_scale(__uint_as_float(top));
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float2 v[4];
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
                                                                   int8_t* __restrict__ codes, long long ld,
                                                                   float* __restrict__ scales) {
     using S = RowSpan<1024, 1, VEC>;
-    __shared__ uint32_t buf[32];
+    __shared__ __align__(16) uint32_t buf[32];
     const size_t m = blockIdx.x;
     const uint16_t* x = X + m * C;
     pdl_wait();
@@ -174,8 +192,9 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
 #pragma unroll
         for (int i = 0; i < 4; ++i) t = max_abs(t, v[i]);
     }
-    const RowScale sc = row_scale(__uint_as_float(block_max_bits<1024>(__float_as_uint(t), buf)));
-    if (threadIdx.x == 0) scales[m] = sc.scale;
+    t = __uint_as_float(block_max_bits<1024>(__float_as_uint(t), buf));
+    const RowCodes sc = row_codes(t);
+    if (threadIdx.x == 0) scales[m] = row_scale(t);
 #pragma unroll 2
     for (int c = 0; c < C; c += 8192) {
         float2 v[4];

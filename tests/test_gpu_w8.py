@@ -77,8 +77,8 @@ def test_quantize_rows(cuda_device, R, C, folded):
     assert codes.shape == (R, C) and codes.stride(0) % 16 == 0
     v = X.float() * ch if folded else X.float()
     q, s = ref.quantize_rows(v.double())
-    # inv is within 2^-23 of 127 / max: at most 127 * 2^-23 beyond half a code; bf16 rows are exact
-    assert ((codes.double() - q).abs() <= 0.5 + (127 * 2.0 ** -23 if folded else 0)).all()
+    # inv is within 2^-21 of 127 / max: at most 127 * 2^-21 beyond half a code; bf16 rows are exact
+    assert ((codes.double() - q).abs() <= 0.5 + (127 * 2.0 ** -21 if folded else 0)).all()
     if not folded:
         assert torch.equal(codes.double(), torch.round(q))
     assert ((scales.double() - s).abs() <= 2.0 ** -24 * s).all()

@@ -11,26 +11,21 @@ import gemv_w4a16_groupwise_b200 as w4
 import w8_reference as ref
 
 
-def _round_up_f32(num, den):
-    """num / den rounded up to fp32 (positive, normal)."""
-    q = np.float32(num / den)
-    return q if Fraction(float(q)) >= Fraction(num, den) else np.nextafter(q, np.float32(np.inf))
-
-
 def test_rounding_rule_is_the_exact_quotient_half_to_even():
-    """rint(v * inv) with inv = 127 / max rounded up equals the exact 127 v / max
-    rounded half to even, for every bf16 significand pair and distance that can matter."""
-    i = np.arange(0, 256)
+    """rint(v * inv) equals the exact 127 v / max rounded half to even for every bf16
+    significand pair and distance that can matter, at both ends of what inv may be:
+    127 / max itself and 2^-21 above it (exactly 127 / max where that is a power of two)."""
+    i, d = np.meshgrid(np.arange(256), np.arange(11))
     for b in range(128, 256):
-        inv = float(_round_up_f32(127, b))
-        for d in range(0, 11):
-            v = i[(i * 2.0 ** -d) <= b] * 2.0 ** -d
-            got = np.rint(v * inv)                  # an fma onto 1.5 * 2^23 rounds the exact product
-            num = np.round(v * 2 ** d).astype(np.int64) * 127
-            den = b * 2 ** d
-            lo, rem2 = num // den, 2 * (num % den)
-            want = lo + ((rem2 > den) | ((rem2 == den) & (lo % 2 == 1)))
-            assert (got == want).all(), (b, d)
+        inside = i <= b * 2 ** d
+        num, den = 127 * i[inside], b * 2 ** d[inside]
+        lo, rem2 = num // den, 2 * (num % den)
+        want = lo + ((rem2 > den) | ((rem2 == den) & (lo % 2 == 1)))
+        exact = np.float64(127) / b
+        up = np.nextafter(exact, 2.0) if Fraction(float(exact)) < Fraction(127, b) else exact
+        for inv in ([exact] if b == 254 else [up, exact * (1 + 2.0 ** -21)]):
+            got = np.rint(i[inside] * 2.0 ** -d[inside] * inv)     # an fma onto 1.5 * 2^23 rounds the exact product
+            assert (got == want).all(), b
 
 
 def _loss(x, y, pre, post, gate, alpha, off, cn, cr):
