@@ -139,7 +139,10 @@ __device__ __forceinline__ float max_abs(float m, float2 v) {
         : "f"(v.x), "f"(v.y));
     return m;
 }
-// the larger magnitudes of two pairs of bf16, as bits
-__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+// the larger magnitudes of two pairs of bf16, a NaN kept
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&m), __habs2(*reinterpret_cast<__nv_bfloat162*>(&w)));
+    return bf162_bits(r);
+}
 
 }  // namespace w4

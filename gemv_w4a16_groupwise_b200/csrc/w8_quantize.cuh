@@ -120,7 +120,7 @@ __device__ __forceinline__ void channel_values(float2 (&v)[4], uint4 x, const fl
 // Rows of at most 16384: a block holds a row in registers between the maximum
 // and the codes, so the row is read once, and has the next row's loads under
 // way meanwhile.  Bound by device memory (3 bytes an element).  The channel
-// factors (twice a row's bytes) come from L1 every time.
+// factors (twice a row's bytes) come from L1, once a row.
 template <int T, int G, int VEC, bool CHANNEL>
 __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
                                                                     const float* __restrict__ channel,
@@ -142,14 +142,14 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
             if (more) next[g] = S::load(X + static_cast<size_t>(m + gridDim.x) * C, g, C);
         }
         uint32_t top;
+        float2 v[CHANNEL ? G : 1][4];       // products with the factors are kept, plain values unpacked again
         if constexpr (CHANNEL) {
             float t = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                float2 v[4];
-                channel_values<S, VEC>(v, x[g], channel, g, C);
+                channel_values<S, VEC>(v[g], x[g], channel, g, C);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) t = max_abs(t, v[i]);
+                for (int i = 0; i < 4; ++i) t = max_abs(t, v[g][i]);
             }
             top = __float_as_uint(t);
         } else {
@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
         if (threadIdx.x == 0) scales[m] = row_scale(__uint_as_float(top));
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float2 v[4];
-            channel_values<S, VEC>(v, x[g], CHANNEL ? channel : nullptr, g, C);
-            store_codes<S, VEC>(codes + static_cast<size_t>(m) * ld, g, C, codes8(v, sc));
+            float2(&u)[4] = v[CHANNEL ? g : 0];
+            if constexpr (!CHANNEL) channel_values<S, VEC>(u, x[g], nullptr, g, C);
+            store_codes<S, VEC>(codes + static_cast<size_t>(m) * ld, g, C, codes8(u, sc));
         }
     }
 }
