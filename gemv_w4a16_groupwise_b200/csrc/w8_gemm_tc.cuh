@@ -69,29 +69,58 @@ __device__ __forceinline__ uint32_t first_cta_addr(const void* p) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
-// 2-D load into this CTA's shared memory that completes on the pair's first CTA's barrier.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+// The producer and the MMA issuer run as whole warps whose lanes hold the same
+// operands, with one elected lane issuing: the operands then sit in uniform
+// registers, where these instructions take them from.  Issued from a branch of
+// one lane, moving them there took 320 cycles for a stage's four MMAs and as
+// much for its two copies, and a stage 600 cycles whatever its tile.
+
+// One 2-D load into this CTA's shared memory that completes on the barrier
+// `bar` of the pair's first CTA; with `expect` that CTA's barrier (its own, at
+// local_bar) is armed first for that many bytes.
+__device__ __forceinline__ void tma_pair_elected(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar,
+                                                 uint32_t local_bar, uint32_t expect) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        "{\n .reg .pred P, L;\n elect.sync _|P, 0xffffffff;\n setp.ne.and.u32 L, %6, 0, P;\n"
+        " @L mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n"
+        " @P cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "r"(local_bar), "r"(expect)
         : "memory");
 }
-__device__ __forceinline__ void umma_i8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The four MMAs of a stage (128 of the reduction), with descriptors `astep`
+// and 2 sixteen-byte units apart, and the release of the stage (`empty`) in
+// both CTAs once they are done.  `accumulate` = 0: the first overwrites.
+__device__ __forceinline__ void umma_i8_stage_elected(uint32_t d, uint64_t adesc, uint64_t bdesc, uint64_t astep,
+                                                      uint32_t idesc, uint32_t accumulate, uint32_t empty) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred P, p;\n .reg .b64 a, b;\n .reg .b16 m;\n"
+        " elect.sync _|P, 0xffffffff;\n setp.ne.b32 p, %5, 0;\n mov.b16 m, 3;\n"
+        " @P tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %4, p;\n"
+        " setp.eq.b32 p, 0, 0;\n"
+        " add.s64 a, %1, %3;\n add.s64 b, %2, 2;\n"
+        " @P tcgen05.mma.cta_group::2.kind::i8 [%0], a, b, %4, p;\n"
+        " add.s64 a, a, %3;\n add.s64 b, b, 2;\n"
+        " @P tcgen05.mma.cta_group::2.kind::i8 [%0], a, b, %4, p;\n"
+        " add.s64 a, a, %3;\n add.s64 b, b, 2;\n"
+        " @P tcgen05.mma.cta_group::2.kind::i8 [%0], a, b, %4, p;\n"
+        " @P tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n}\n" ::"r"(
+            d),
+        "l"(adesc), "l"(bdesc), "l"(astep), "r"(idesc), "r"(accumulate), "r"(empty)
         : "memory");
 }
 // Arrive on the barrier at this offset in both CTAs once the MMAs before are done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void umma_commit_pair_elected(uint32_t bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "{\n .reg .pred P;\n .reg .b16 m;\n elect.sync _|P, 0xffffffff;\n mov.b16 m, 3;\n"
+        " @P tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
+            bar)
         : "memory");
+}
+// mbar_wait_bounded by a whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                  unsigned int err) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort, err));
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -212,96 +241,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
 
     W8Walk walk(a, pair, pairs);
     W8Unit u;
-    auto load_weights = [&](int s, int kb, int o0) {
-        uint8_t* st = base + s * kStageBytes;
-        const uint32_t bar = first_cta_addr(&full[s]);
-        if (TR) tma_load_2d_pair(st, &wmap, o0, kb * kW8Red, bar);
-        else tma_load_2d_pair(st, &wmap, kb * kW8Red, o0, bar);
-    };
+    const uint32_t stage0 = smem_u32(base), full0 = smem_u32(full), empty0 = smem_u32(empty);
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int s = 0;
-            uint32_t round = 0;
-            bool ok = true;
-            // Weights that no kernel still running writes (a.early) are asked
-            // for before the tokens' codes are waited for: the first NS stages.
-            int early = 0;
-            if (a.early) {
-                W8Walk ahead(a, pair, pairs);
-                while (early < NS && ahead.next(&u)) {
-                    const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
-                    for (int kb = u.kb0; kb < u.kb1 && early < NS; ++kb, ++early) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[early], 2 * kStageBytes);
-                        load_weights(early, kb, o0);
-                    }
-                }
-            }
-            pdl_wait();
-            int n = 0;
-            while (ok && walk.next(&u)) {
-                const int m0 = (u.tile % a.tiles_m) * TN + static_cast<int>(rank) * (TN / 2);
+        const uint32_t full_first = first_cta_addr(full);
+        const uint32_t expect = rank == 0 ? 2 * kStageBytes : 0;
+        auto load_weights = [&](int s, int kb, int o0) {
+            tma_pair_elected(stage0 + s * kStageBytes, &wmap, TR ? o0 : kb * kW8Red, TR ? kb * kW8Red : o0,
+                             full_first + 8 * s, full0 + 8 * s, expect);
+        };
+        int s = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        // Weights that no kernel still running writes (a.early) are asked for
+        // before the tokens' codes are waited for: the first NS stages.
+        int early = 0;
+        if (a.early) {
+            W8Walk ahead(a, pair, pairs);
+            while (early < NS && ahead.next(&u)) {
                 const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
-                for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
-                    if (round > 0 && !mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty)) {
-                        ok = false;
-                        break;
-                    }
-                    if (n >= early) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                        load_weights(s, kb, o0);
-                    }
-                    tma_load_2d_pair(base + s * kStageBytes + kW8ABytes, &amap, kb * kW8Red, m0,
-                                     first_cta_addr(&full[s]));
-                    if (++s == NS) {
-                        s = 0;
-                        ++round;
-                    }
-                }
+                for (int kb = u.kb0; kb < u.kb1 && early < NS; ++kb, ++early) load_weights(early, kb, o0);
             }
-            // the releases of the stages still in use come from the other CTA:
-            // see them in before this one may leave
-            for (int j = 0; j < NS && ok; ++j) {
-                if (round > 0) ok = mbar_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty);
+        }
+        pdl_wait();
+        int n = 0;
+        while (ok && walk.next(&u)) {
+            const int m0 = (u.tile % a.tiles_m) * TN + static_cast<int>(rank) * (TN / 2);
+            const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
+            for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
+                if (round > 0 && !warp_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty)) {
+                    ok = false;
+                    break;
+                }
+                if (n >= early) load_weights(s, kb, o0);
+                tma_pair_elected(stage0 + s * kStageBytes + kW8ABytes, &amap, kb * kW8Red, m0, full_first + 8 * s,
+                                 full0 + 8 * s, 0);
                 if (++s == NS) {
                     s = 0;
                     ++round;
                 }
             }
         }
+        // the releases of the stages still in use come from the other CTA:
+        // see them in before this one may leave
+        for (int j = 0; j < NS && ok; ++j) {
+            if (round > 0) ok = warp_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty);
+            if (++s == NS) {
+                s = 0;
+                ++round;
+            }
+        }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            // MN-major: 32 reduction rows are four groups of 8 rows, 1024 bytes each
+            const uint64_t adesc0 = TR ? umma_desc_sw128(stage0, kW8ABytes, 1024) : umma_desc_sw128(stage0, 16, 1024);
+            const uint64_t bdesc0 = umma_desc_sw128(stage0 + kW8ABytes, 16, 1024);
             bool ok = true;
             int s = 0, i = 0;
             uint32_t phase = 0;
             while (ok && walk.next(&u)) {
                 const int buf = i & 1;
-                if (i >= 2) ok = mbar_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1u, abort_flag, kErrTimeoutAccum);
+                if (i >= 2) ok = warp_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1u, abort_flag, kErrTimeoutAccum);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem_d + static_cast<uint32_t>(buf) * TN;
                 for (int kb = u.kb0; kb < u.kb1; ++kb) {
-                    ok = mbar_wait_bounded(&full[s], phase, abort_flag, kErrTimeoutTmaFull);
+                    ok = warp_wait_bounded(&full[s], phase, abort_flag, kErrTimeoutTmaFull);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(base + s * kStageBytes);
-                    const uint32_t b_addr = a_addr + kW8ABytes;
-#pragma unroll
-                    for (int j = 0; j < kW8Red / 32; ++j) {
-                        // MN-major: 32 reduction rows are four groups of 8 rows, 1024 bytes each
-                        const uint64_t adesc = TR ? umma_desc_sw128(a_addr + j * 4096, kW8ABytes, 1024)
-                                                  : umma_desc_sw128(a_addr + j * 32, 16, 1024);
-                        const uint64_t bdesc = umma_desc_sw128(b_addr + j * 32, 16, 1024);
-                        umma_i8_pair(acc, adesc, bdesc, kIdesc, (kb != u.kb0 || j != 0) ? 1u : 0u);
-                    }
-                    umma_commit_pair(&empty[s]);
+                    const uint64_t at = static_cast<uint64_t>(s * (kStageBytes >> 4));
+                    umma_i8_stage_elected(tmem_d + static_cast<uint32_t>(buf) * TN, adesc0 + at, bdesc0 + at,
+                                          TR ? 4096 >> 4 : 32 >> 4, kIdesc, kb != u.kb0 ? 1u : 0u, empty0 + 8 * s);
                     if (++s == NS) {
                         s = 0;
                         phase ^= 1u;
                     }
                 }
-                umma_commit_pair(&acc_full[buf]);   // also tracks any MMA issued before an abort
+                // also tracks any MMA issued before an abort
+                umma_commit_pair_elected(smem_u32(&acc_full[buf]));
                 ++i;
             }
         }
@@ -402,10 +419,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         }
     }
 
-    // The lanes of a warp whose lane 0 alone had a role come together here:
-    // the collective instructions below take whole warps, and a deallocation
-    // that each part of a split warp issued would free the tensor memory of
-    // whatever runs on the SM next.
+    // The collective instructions below take whole warps: a deallocation that
+    // each part of a split warp issued would free the tensor memory of whatever
+    // runs on the SM next.
     __syncwarp();
     tc_fence_before();
     __syncthreads();
