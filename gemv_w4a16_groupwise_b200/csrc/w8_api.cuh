@@ -56,27 +56,52 @@ w4_status run_quantize_rows(const uint16_t* X, int R, int C, const float* channe
 struct W8Plan {
     int TN = 32, tiles_m = 1, tiles = 1, F = 0, chunks = 1, cut_pairs = 1, grid_pairs = 1;
     size_t ws = 0;
+    double us = 0.0;     // the estimate it was chosen by
 };
 
-W8Plan plan_w8(int M, int N, int K, bool transposed, int sms) {
+// A plan's time by what was measured on 74 pairs: a call with one stage per
+// tile takes `base`; every further stage of a pair adds `stage` (0.275 us for
+// 256 tokens is the products' time, the others wait for the 16 KB of weights
+// and their tokens from L2); a call is not faster than its weights through
+// device memory; partial tiles, their sums and the second kernel add `cut`.
+// (us)               TN =    32     64    128    256
+constexpr double kW8Base[] = {4.6, 4.8, 5.5, 6.5};
+constexpr double kW8Stage[] = {0.175, 0.18, 0.20, 0.275};
+constexpr double kW8Cut[] = {4.2, 4.5, 9.0, 11.0};
+
+W8Plan plan_w8_as(int M, int N, int K, bool transposed, int pairs, int size, bool cut) {
     W8Plan p;
     const int out = transposed ? K : N, red = transposed ? N : K;
-    p.TN = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    p.TN = 32 << size;
     p.tiles_m = (M + p.TN - 1) / p.TN;
     p.tiles = p.tiles_m * ((out + w4::kW8Rows - 1) / w4::kW8Rows);
     p.chunks = (red + w4::kW8Red - 1) / w4::kW8Red;
-    const int pairs = std::max(1, sms / 2);
-    const int rem = p.tiles % pairs;
-    // a last wave that is nearly full runs as whole tiles; an emptier one is
-    // cut over all pairs, at least 4 stages each
-    p.F = rem * 4 > pairs * 3 ? p.tiles : p.tiles - rem;
+    p.F = cut ? p.tiles - p.tiles % pairs : p.tiles;
     const long long total = static_cast<long long>(p.tiles - p.F) * p.chunks;
     p.cut_pairs = static_cast<int>(std::max<long long>(1, std::min<long long>(pairs, total / 4)));
     p.grid_pairs = std::max(std::min(p.F, pairs), total > 0 ? p.cut_pairs : 1);
-    // one pair per tile leaves nothing to add up
-    p.ws = p.cut_pairs > 1 && total > 0
-               ? static_cast<size_t>(2) * p.cut_pairs * p.TN * w4::kW8Rows * sizeof(int32_t) : 0;
+    // one pair leaves nothing to add up
+    const bool partials = total > 0 && p.cut_pairs > 1;
+    if (partials) p.ws = static_cast<size_t>(2) * p.cut_pairs * p.TN * w4::kW8Rows * sizeof(int32_t);
+    const double stages = static_cast<double>((p.F + pairs - 1) / pairs) * p.chunks +
+                          static_cast<double>(total) / p.cut_pairs;
+    p.us = std::max(kW8Base[size] + stages * kW8Stage[size],
+                    static_cast<double>(N) * K / 6.3e6 + 3.5) + (partials ? kW8Cut[size] : 0.0);
     return p;
+}
+
+W8Plan plan_w8(int M, int N, int K, bool transposed, int sms) {
+    const int pairs = std::max(1, sms / 2);
+    W8Plan best;
+    best.us = 1e30;
+    for (int size = 0; size < 4; ++size) {
+        for (int cut = 0; cut < 2; ++cut) {
+            const W8Plan p = plan_w8_as(M, N, K, transposed, pairs, size, cut != 0);
+            if (p.us < best.us) best = p;
+        }
+        if (M <= (32 << size)) break;    // a wider tile would only be emptier
+    }
+    return best;
 }
 
 // int8 rows, `ld` bytes apart, in boxes of 128 bytes x box_rows with the
@@ -115,8 +140,12 @@ w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, bool
     return launch_status();
 }
 
-// The stream kernel serves forward products of a few tokens.
-bool w8_gemv_serves(int M, bool transposed) { return !transposed && M <= w4::kGvMaxTokens; }
+// The stream kernel serves forward products of a few tokens whose codes it can
+// hold (8 tokens as far as K = 6656).
+bool w8_gemv_serves(int M, int K, bool transposed) {
+    return !transposed && M <= w4::kGvMaxTokens &&
+           static_cast<long long>(M) * w4::w8_gemv_token_bytes(K) <= w4::kGvCodeBytes;
+}
 
 // Whether w8_gemv_kernel quantizes the tokens itself, and for how many at
 // once (1, 2 or 4; 0: it does not): rows of whole 16 bytes, at most
@@ -131,12 +160,15 @@ template <int MT>
 w4_status launch_w8_gemv(const w4::W8Args& p, const uint16_t* X, cudaStream_t st) {
     const w4::W8GemvArgs a = {p, X};
     const size_t smem =
-        MT > 0 ? static_cast<size_t>(MT) * w4::w8_gemv_token_bytes(p.K) + 2 * w4::kGvFusedValues : 0;
+        static_cast<size_t>(MT > 0 ? MT : p.M) * w4::w8_gemv_token_bytes(p.K) + (MT > 0 ? 2 * w4::kGvFusedValues : 0);
     if (smem > 40 * 1024 &&
-        ensure_smem(reinterpret_cast<const void*>(w4::w8_gemv_kernel<MT>), smem) != cudaSuccess)
+        ensure_smem(reinterpret_cast<const void*>(w4::w8_gemv_kernel<MT>), w4::kGvMaxSmem) != cudaSuccess)
         return W4_ERR_CUDA;
-    launch_pdl(w4::w8_gemv_kernel<MT>, dim3((p.N + w4::kGvRows - 1) / w4::kGvRows), dim3(w4::kGvWarps * 32),
-               smem, st, a);
+    // two blocks an SM, with equal shares of the 16-row blocks
+    const int blocks = (p.N + w4::kGvRows - 1) / w4::kGvRows;
+    const int slots = 2 * device_info(current_device()).sms;
+    const int each = (blocks + slots - 1) / slots;
+    launch_pdl(w4::w8_gemv_kernel<MT>, dim3((blocks + each - 1) / each), dim3(w4::kGvWarps * 32), smem, st, a);
     return launch_status();
 }
 
@@ -144,7 +176,7 @@ w4_status launch_w8_gemv(const w4::W8Args& p, const uint16_t* X, cudaStream_t st
 // which does not write the weights and lets its dependents start only after
 // all that came before it.
 w4_status run_w8_gemm(const w4::W8Args& a, bool transposed, void* ws, bool early, cudaStream_t st) {
-    if (w8_gemv_serves(a.M, transposed)) return launch_w8_gemv<0>(a, nullptr, st);
+    if (w8_gemv_serves(a.M, a.K, transposed)) return launch_w8_gemv<0>(a, nullptr, st);
     const DeviceInfo di = device_info(current_device());
     const W8Plan p = plan_w8(a.M, a.N, a.K, transposed, di.sms);
     int32_t* part = static_cast<int32_t*>(ws);
@@ -178,7 +210,7 @@ w4_status w8_quantize_rows(const void* X, int R, int C, const float* channel_sca
 }
 
 size_t w8a8_workspace_bytes(int M, int N, int K, int transposed) {
-    if (M <= 0 || N <= 0 || K <= 0 || w8_gemv_serves(M, transposed != 0)) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || w8_gemv_serves(M, K, transposed != 0)) return 0;
     return plan_w8(M, N, K, transposed != 0, device_info(current_device()).sms).ws;
 }
 

@@ -1,18 +1,20 @@
 // Small-batch forward product (M <= 8): Y = A . W^T with int8 codes.
 //
 // Bound by the weights' bytes, so the kernel is a stream with little in its
-// way: a block takes 16 weight rows, its 8 warps interleaved 64-byte pieces of
-// them, and every lane has 16 loads of 16 bytes under way before the first is
-// used (two blocks of an SM: 128 KB in flight).  The loads land where
+// way: a block takes 16 weight rows at a time, its 8 warps interleaved 64-byte
+// pieces of them, and every lane has 16 loads of 16 bytes under way (two blocks
+// of an SM: 128 KB in flight): the next ones are asked for as soon as the
+// products have taken the last, before the sums of a finished 16 rows are
+// added up.  The loads land where
 // mma.sync.m16n8k32 wants them: lane (g, t) holds bytes 16 t .. 16 t + 15 of a
 // piece of rows g and g + 8, and of token g; that the four words stand for
 // other k than the instruction's own order is the same on both sides.  The
 // integer sums of the warps are added in shared memory.
 //
-// MT > 0: bf16 tokens, quantized by every block for itself while the first
+// MT > 0: bf16 tokens, quantized by every block for itself while its first
 // weights are on their way (up to 16384 values a block, from L2): one launch
 // for a decoding step's layer instead of two, and no codes through memory.
-// MT = 0: the tokens' codes come from memory.
+// MT = 0: the tokens' codes are copied to shared memory.
 #pragma once
 
 #include "w8_gemm.cuh"
@@ -21,6 +23,11 @@
 namespace w4 {
 
 constexpr int kGvRows = 16, kGvWarps = 8, kGvUnroll = 8, kGvMaxTokens = 8;
+// Bytes of the tokens' codes that a block takes into shared memory.  Past that
+// (4 tokens of 14336) the copying in front of every block costs more than the
+// tensor-core product's fixed time: 18.6 us against 17 at 4096 x 14336.
+constexpr int kGvCodeBytes = 56 * 1024;
+constexpr int kGvMaxSmem = 64 * 1024;
 constexpr int kGvFusedValues = 16384;      // MT * K that a block may quantize for itself: 32 KB of bf16
 
 // Bytes of a token's codes in shared memory: whole 512-byte steps of the
@@ -62,16 +69,13 @@ __device__ __forceinline__ uint4 mask_tail(uint4 v, int k, int K) {
 
 template <int MT>
 __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvArgs a) {
-    extern __shared__ __align__(16) uint8_t tokens[];      // MT rows of w8_gemv_token_bytes(K), then bf16
-    __shared__ int red[kGvWarps][kGvMaxTokens][kGvRows];
+    extern __shared__ __align__(16) uint8_t tokens[];      // rows of w8_gemv_token_bytes(K); MT > 0: then bf16
+    __shared__ int red[2][kGvWarps][kGvMaxTokens][kGvRows];
     __shared__ uint32_t tops[kGvWarps];
     __shared__ float token_scale[kGvMaxTokens];
     const int K = a.p.K, N = a.p.N, M = a.p.M;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int r0 = blockIdx.x * kGvRows;
-    // rows past N repeat the last one; their sums are dropped
-    const int8_t* w_lo = a.p.W + static_cast<size_t>(min(r0 + g, N - 1)) * a.p.ldw;
-    const int8_t* w_hi = a.p.W + static_cast<size_t>(min(r0 + g + 8, N - 1)) * a.p.ldw;
+    const int blocks = (N + kGvRows - 1) / kGvRows;
     const int k_first = 64 * warp + 16 * t;                // then every 512
     pdl_launch_dependents();
     pdl_wait();
@@ -92,7 +96,10 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
     }
 
     uint4 lo[kGvUnroll], hi[kGvUnroll];
-    auto load = [&](int k0) {
+    auto load = [&](int b, int k0) {
+        // rows past N repeat the last one; their sums are dropped
+        const int8_t* w_lo = a.p.W + static_cast<size_t>(min(b * kGvRows + g, N - 1)) * a.p.ldw;
+        const int8_t* w_hi = a.p.W + static_cast<size_t>(min(b * kGvRows + g + 8, N - 1)) * a.p.ldw;
 #pragma unroll
         for (int i = 0; i < kGvUnroll; ++i) {
             const int k = k0 + 512 * i;
@@ -103,7 +110,7 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
             }
         }
     };
-    load(k_first);
+    load(blockIdx.x, k_first);
 
     if constexpr (MT > 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");   // every thread reads back what it copied
@@ -136,39 +143,57 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
         __syncthreads();
     }
 
+    if constexpr (MT == 0) {
+        // the codes, and zeros up to the end of the block's last step
+        for (int m = 0; m < M; ++m)
+            for (int k = threadIdx.x * 16; k < tb - 64; k += kGvWarps * 32 * 16) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (k < K) x = *reinterpret_cast<const uint4*>(a.p.A + static_cast<size_t>(m) * a.p.lda + k);
+                if (k + 16 > K) x = mask_tail(x, k, K);
+                *reinterpret_cast<uint4*>(tokens + m * tb + k) = x;
+            }
+        __syncthreads();
+    }
+    const int held = MT > 0 ? MT : M;      // tokens in shared memory
+
     int c[4] = {0, 0, 0, 0};
-    for (int k0 = k_first; k0 - 16 * t < K; k0 += 512 * kGvUnroll) {
-        if (k0 != k_first) load(k0);
+    int turn = 0;
+    int k0 = k_first;
+    for (int b = blockIdx.x; b < blocks;) {
 #pragma unroll
         for (int i = 0; i < kGvUnroll; ++i) {
             const int k = k0 + 512 * i;
             if (k - 16 * t >= K) break;                    // the warp's piece lies behind the row
-            uint4 b = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (MT > 0) {
-                if (g < MT) b = *reinterpret_cast<const uint4*>(tokens + g * tb + k);
-            } else {
-                if (g < M && k < K) {
-                    b = *reinterpret_cast<const uint4*>(a.p.A + static_cast<size_t>(g) * a.p.lda + k);
-                    if (k + 16 > K) b = mask_tail(b, k, K);
-                }
-            }
-            mma_s8(c, lo[i].x, hi[i].x, lo[i].y, hi[i].y, b.x, b.y);
-            mma_s8(c, lo[i].z, hi[i].z, lo[i].w, hi[i].w, b.z, b.w);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (g < held) x = *reinterpret_cast<const uint4*>(tokens + g * tb + k);
+            mma_s8(c, lo[i].x, hi[i].x, lo[i].y, hi[i].y, x.x, x.y);
+            mma_s8(c, lo[i].z, hi[i].z, lo[i].w, hi[i].w, x.z, x.w);
         }
-    }
-    red[warp][2 * t][g] = c[0];
-    red[warp][2 * t + 1][g] = c[1];
-    red[warp][2 * t][g + 8] = c[2];
-    red[warp][2 * t + 1][g + 8] = c[3];
-    __syncthreads();
-    const int m = threadIdx.x / kGvRows, r = threadIdx.x % kGvRows, n = r0 + r;
-    if (m < M && n < N) {
-        int s = 0;
+        k0 += 512 * kGvUnroll;
+        const bool done = k0 - k_first >= (K + 511) / 512 * 512;       // the same in every warp
+        const int here = b;
+        if (done) {
+            b += gridDim.x;
+            k0 = k_first;
+        }
+        if (b < blocks) load(b, k0);
+        if (!done) continue;
+        red[turn][warp][2 * t][g] = c[0];
+        red[turn][warp][2 * t + 1][g] = c[1];
+        red[turn][warp][2 * t][g + 8] = c[2];
+        red[turn][warp][2 * t + 1][g + 8] = c[3];
+        c[0] = c[1] = c[2] = c[3] = 0;
+        __syncthreads();
+        const int m = threadIdx.x / kGvRows, r = threadIdx.x % kGvRows, n = here * kGvRows + r;
+        if (m < M && n < N) {
+            int s = 0;
 #pragma unroll
-        for (int w = 0; w < kGvWarps; ++w) s += red[w][m][r];
-        const float as = MT > 0 ? token_scale[m] : a.p.a_scales[m];
-        a.p.Y[static_cast<size_t>(m) * N + n] =
-            w8_output(s, as * a.p.w_scales[n], a.p.bias ? bf16_bits_to_float(a.p.bias[n]) : 0.0f);
+            for (int w = 0; w < kGvWarps; ++w) s += red[turn][w][m][r];
+            const float as = MT > 0 ? token_scale[m] : a.p.a_scales[m];
+            a.p.Y[static_cast<size_t>(m) * N + n] =
+                w8_output(s, as * a.p.w_scales[n], a.p.bias ? bf16_bits_to_float(a.p.bias[n]) : 0.0f);
+        }
+        turn ^= 1;
     }
 }
 
