@@ -458,6 +458,10 @@ def _check_first(t, name):
     """The bf16 matrix that a call is about; returns its device's index."""
     if _Torch.torch is None:
         _Torch.load()
+    if t.__class__ is _Torch.torch.Tensor and t.dtype is _Torch.bf16 and t.dim() == 2 and t.is_contiguous():
+        dev = t.get_device()
+        if dev >= 0:
+            return dev
     _check_cuda(t, name, _Torch.bf16)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
@@ -496,7 +500,7 @@ def _check_codes(t, name, dev=None, rows=None, cols=None) -> int:
 
 def _empty_codes(like, R: int, C: int):
     C16 = (C + 15) // 16 * 16
-    q = like.new_empty((R, C16), dtype=_Torch.i8)
+    q = like.new_empty(R, C16, dtype=_Torch.i8)
     return q if C16 == C else q[:, :C]
 
 
@@ -512,7 +516,7 @@ def w8_quantize_rows(X, channel_scales=None, out=None):
     if channel_scales is not None:
         _check_rows(channel_scales, "channel_scales", _Torch.f32, dev, (C,))
     if out is None:
-        codes, scales = _empty_codes(X, R, C), X.new_empty((R,), dtype=_Torch.f32)
+        codes, scales = _empty_codes(X, R, C), X.new_empty(R, dtype=_Torch.f32)
         ld = (C + 15) // 16 * 16
     else:
         codes, scales = out
@@ -535,7 +539,7 @@ def _w8_operands(A, dev, codes, scales, bias, transposed, out):
     if bias is not None:
         _check_rows(bias, "bias", _Torch.bf16, dev, (out_len,))
     if out is None:
-        out = A.new_empty((M, out_len), dtype=_Torch.bf16)
+        out = A.new_empty(M, out_len, dtype=_Torch.bf16)
     else:
         _check_rows(out, "out", _Torch.bf16, dev, (M, out_len))
     return M, N, K, ldw, out
@@ -551,7 +555,7 @@ def _w8_workspace(query, dev, M, N, K, transposed, like):
         if len(_ws_cache) > 4096:
             _ws_cache.clear()
         _ws_cache[key] = n
-    return (like.new_empty((n,), dtype=_Torch.u8) if n else None), n
+    return (like.new_empty(n, dtype=_Torch.u8) if n else None), n
 
 
 def w8a8_gemm(A, a_scales, codes, scales=None, *, bias=None, transposed: bool = False, out=None):
@@ -660,10 +664,10 @@ def w4_block_norm(x, y=None, *, pre_weight, post_weight=None, gate=None, residua
         _check_rows(residual_out, "residual_out", _Torch.bf16, dev, (M, C))
         residual = residual_out
     if quantize:
-        normed, scales = _empty_codes(x, M, C), x.new_empty((M,), dtype=_Torch.f32)
+        normed, scales = _empty_codes(x, M, C), x.new_empty(M, dtype=_Torch.f32)
     else:
         normed, scales = _Torch.empty_like(x), None
-    rstd = x.new_empty((2, M), dtype=_Torch.f32) if keep_rstd else None
+    rstd = x.new_empty(2, M, dtype=_Torch.f32) if keep_rstd else None
     _call("w4_block_norm", dev, x.data_ptr(), _ptr(y), M, C, _ptr(post_weight), _ptr(gate), kind, residual_scale,
           pre_weight.data_ptr(), weight_offset, eps, None if y is None else residual.data_ptr(), normed.data_ptr(),
           (C + 15) // 16 * 16, _ptr(scales), _ptr(rstd))
@@ -695,7 +699,7 @@ def w4_block_norm_backward(d_normed, residual, rstd, y=None, *, d_residual=None,
     if nws is None:
         with _OnDevice(dev):
             nws = _ws_cache[key] = int(_Torch.lib.w4_block_norm_workspace_bytes(M, C))
-    ws = d_x.new_empty((nws,), dtype=_Torch.u8)
+    ws = d_x.new_empty(nws, dtype=_Torch.u8)
     _call("w4_block_norm_backward", dev, d_normed.data_ptr(), _ptr(d_residual), residual.data_ptr(), rstd.data_ptr(),
           _ptr(y), M, C, _ptr(post_weight), _ptr(gate), kind, residual_scale, pre_weight.data_ptr(), weight_offset,
           d_x.data_ptr(), _ptr(d_y), d_pre.data_ptr(), _ptr(d_post), _ptr(d_gate), ws.data_ptr(), nws)
