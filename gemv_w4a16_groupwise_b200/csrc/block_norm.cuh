@@ -55,24 +55,27 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
     __shared__ __align__(16) uint32_t ubuf[2][32];
     const float inv_c = 1.0f / static_cast<float>(a.C);
     const bool post = a.post != nullptr, token = a.gate_kind == kGateToken, gated = a.gate_kind != kGateNone;
-    const RowPipe<T, G, VEC, VEC == 8> pipe = {ring, 1 + (a.y ? 1 : 0) + (token ? 1 : 0), a.C};
+    const S span(blockIdx.x, a.C);
+    const RowPipe<T, G, VEC, true> pipe = {ring, 1 + (a.y ? 1 : 0) + (token ? 1 : 0), span};
     pdl_launch_dependents();
     pdl_wait();
     auto fetch = [&](int stage, long long m) {
-        const size_t at = static_cast<size_t>(m) * a.C;
-        pipe.fetch(stage, 0, a.x + at);
-        if (a.y) pipe.fetch(stage, 1, a.y + at);
-        if (token) pipe.fetch(stage, 2, a.gate + at);
+        const int C = fresh(a.C);
+        const size_t at = static_cast<size_t>(m) * C;
+        pipe.fetch(stage, 0, a.x + at, C);
+        if (a.y) pipe.fetch(stage, 1, a.y + at, C);
+        if (token) pipe.fetch(stage, 2, a.gate + at, C);
         pipe.commit();
     };
     fetch(0, blockIdx.x);
     const float2 off = both(a.off);
     uint4 wpre[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) wpre[g] = S::load(a.pre, g, a.C);
+    for (int g = 0; g < G; ++g) wpre[g] = span.load_vector(a.pre, g, a.C);
     int turn = 0;
     for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
-        const size_t at = static_cast<size_t>(m) * a.C;
+        const int C = VEC == 8 ? a.C : fresh(a.C);
+        const size_t at = static_cast<size_t>(m) * C;
         const bool more = m + gridDim.x < a.M;
         if (more) fetch(turn ^ 1, m + gridDim.x);
         pipe.wait(more);
@@ -81,7 +84,7 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
             float2 ss = both(0.0f);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const uint4 y = pipe.read(turn, 1, a.y + at, g);
+                const uint4 y = pipe.read(turn, 1, a.y + at, g, C);
                 for (uint32_t w : {y.x, y.y, y.z, y.w}) {
                     const float2 v = unpack_bf16x2(w);
                     ss = ffma2(v, v, ss);
@@ -93,27 +96,27 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
         float2 ss = both(0.0f);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const uint4 x = pipe.read(turn, 0, a.x + at, g);
+            const uint4 x = pipe.read(turn, 0, a.x + at, g, C);
             r[g][0] = x.x, r[g][1] = x.y, r[g][2] = x.z, r[g][3] = x.w;
             if (a.y) {
-                const uint4 y = pipe.read(turn, 1, a.y + at, g);
+                const uint4 y = pipe.read(turn, 1, a.y + at, g, C);
                 float2 t[4] = {unpack_bf16x2(y.x), unpack_bf16x2(y.y), unpack_bf16x2(y.z), unpack_bf16x2(y.w)};
                 if (post) {
-                    const uint4 p = S::load(a.post, g, a.C);
+                    const uint4 p = span.load_vector(a.post, g, C);
                     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         t[i] = fmul2(fmul2(t[i], both(rstd_y)), fadd2(unpack_bf16x2(w[i]), off));
                 }
                 if (gated) {
-                    const uint4 p = token ? pipe.read(turn, 2, a.gate + at, g) : S::load(a.gate, g, a.C);
+                    const uint4 p = token ? pipe.read(turn, 2, a.gate + at, g, C) : span.load_vector(a.gate, g, C);
                     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) t[i] = fmul2(t[i], unpack_bf16x2(w[i]));
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r[g][i] = pack_bf16x2(ffma2(both(a.alpha), t[i], unpack_bf16x2(r[g][i])));
-                S::store(a.residual + at, g, a.C, r[g]);
+                span.store(a.residual + at, g, C, r[g]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
                 if constexpr (CODES) top = max_abs(top, n[g][i]);
                 else r[g][i] = pack_bf16x2(n[g][i]);
             }
-            if constexpr (!CODES) S::store(static_cast<uint16_t*>(a.normed) + at, g, a.C, r[g]);
+            if constexpr (!CODES) span.store(static_cast<uint16_t*>(a.normed) + at, g, C, r[g]);
         }
         if constexpr (CODES) {
             top = __uint_as_float(block_max_bits<T>(__float_as_uint(top), ubuf[turn]));
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
             if (threadIdx.x == 0) a.scales[m] = row_scale(top);
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                store_codes<S, VEC>(static_cast<int8_t*>(a.normed) + static_cast<size_t>(m) * a.ld, g, a.C,
+                store_codes<VEC>(span, static_cast<int8_t*>(a.normed) + static_cast<size_t>(m) * a.ld, g, C,
                                     codes8(n[g], sc));
         }
     }
@@ -182,7 +185,7 @@ __host__ __device__ constexpr int norm_grad_blocks_per_sm(int T, int G) {
 template <int T, int G, int VEC, bool ACC_SMEM>
 __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_backward_kernel(const NormGradArgs a) {
     using S = RowSpan<T, G, VEC>;
-    constexpr bool PIPED = VEC == 8 && !ACC_SMEM;
+    constexpr bool PIPED = !ACC_SMEM;
     constexpr int kRegs = ACC_SMEM ? 1 : G;
     extern __shared__ uint4 dyn_smem[];     // the row pipe; with ACC_SMEM the sums, [sums][G][4][T]
     float2* acc_smem = reinterpret_cast<float2*>(dyn_smem);
@@ -210,34 +213,41 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
         }
     };
     const int dres_at = 2, y_at = 2 + (a.dres ? 1 : 0), gate_at = y_at + (a.y ? 1 : 0);
-    const RowPipe<T, G, VEC, PIPED> pipe = {dyn_smem, gate_at + (token ? 1 : 0), a.C};
+    const S span(blockIdx.x, a.C);
+    const RowPipe<T, G, VEC, PIPED> pipe = {dyn_smem, gate_at + (token ? 1 : 0), span};
     auto fetch = [&](int stage, long long m) {
-        const size_t at = static_cast<size_t>(m) * a.C;
-        pipe.fetch(stage, 0, a.dn + at);
-        pipe.fetch(stage, 1, a.r + at);
-        if (a.dres) pipe.fetch(stage, dres_at, a.dres + at);
-        if (a.y) pipe.fetch(stage, y_at, a.y + at);
-        if (token) pipe.fetch(stage, gate_at, a.gate + at);
+        const int C = fresh(a.C);
+        const size_t at = static_cast<size_t>(m) * C;
+        pipe.fetch(stage, 0, a.dn + at, C);
+        pipe.fetch(stage, 1, a.r + at, C);
+        if (a.dres) pipe.fetch(stage, dres_at, a.dres + at, C);
+        if (a.y) pipe.fetch(stage, y_at, a.y + at, C);
+        if (token) pipe.fetch(stage, gate_at, a.gate + at, C);
         pipe.commit();
     };
     auto words = [](uint4 v, uint32_t (&w)[4]) { w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w; };
     fetch(0, blockIdx.x);
+    float next_rr = a.rstd[a.M + blockIdx.x], next_ry = post ? a.rstd[blockIdx.x] : 1.0f;
     const float2 off = both(a.off);
     int turn = 0;
     for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
-        const size_t at = static_cast<size_t>(m) * a.C;
+        const int C = VEC == 8 ? a.C : fresh(a.C);
+        const size_t at = static_cast<size_t>(m) * C;
         const bool more = m + gridDim.x < a.M;
-        if (more) fetch(turn ^ 1, m + gridDim.x);
-        const float2 rr = both(a.rstd[a.M + m]);
-        const float2 ry = both(post ? a.rstd[m] : 1.0f);
+        const float2 rr = both(next_rr), ry = both(next_ry);
+        if (more) {
+            fetch(turn ^ 1, m + gridDim.x);
+            next_rr = a.rstd[a.M + m + gridDim.x];
+            if (post) next_ry = a.rstd[m + gridDim.x];
+        }
         pipe.wait(more);
         float2 s = both(0.0f);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             uint32_t dn[4], r[4], w[4];
-            words(pipe.read(turn, 0, a.dn + at, g), dn);
-            words(pipe.read(turn, 1, a.r + at, g), r);
-            words(S::load(a.pre, g, a.C), w);
+            words(pipe.read(turn, 0, a.dn + at, g, C), dn);
+            words(pipe.read(turn, 1, a.r + at, g, C), r);
+            words(span.load_vector(a.pre, g, C), w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 xh = fmul2(unpack_bf16x2(r[i]), rr), d = unpack_bf16x2(dn[i]);
@@ -252,9 +262,9 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             uint32_t dn[4], r[4], w[4], dx[4];
-            words(pipe.read(turn, 0, a.dn + at, g), dn);
-            words(pipe.read(turn, 1, a.r + at, g), r);
-            words(S::load(a.pre, g, a.C), w);
+            words(pipe.read(turn, 0, a.dn + at, g, C), dn);
+            words(pipe.read(turn, 1, a.r + at, g, C), r);
+            words(span.load_vector(a.pre, g, C), w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 xh = fmul2(unpack_bf16x2(r[i]), rr);
@@ -262,21 +272,21 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
                 dt[g][i] = ffma2(xh, c1, fmul2(dh, rr));
             }
             if (a.dres) {
-                words(pipe.read(turn, dres_at, a.dres + at, g), w);
+                words(pipe.read(turn, dres_at, a.dres + at, g, C), w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dt[g][i] = fadd2(dt[g][i], unpack_bf16x2(w[i]));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) dx[i] = pack_bf16x2(dt[g][i]);
-            S::store(a.dx + at, g, a.C, dx);
+            span.store(a.dx + at, g, C, dx);
             if (!a.y) continue;
             uint32_t y[4], p[4];
-            words(pipe.read(turn, y_at, a.y + at, g), y);
-            if (post) words(S::load(a.post, g, a.C), p);
+            words(pipe.read(turn, y_at, a.y + at, g, C), y);
+            if (post) words(span.load_vector(a.post, g, C), p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dt[g][i] = fmul2(dt[g][i], both(a.alpha));
             if (chan || token) {
-                words(token ? pipe.read(turn, gate_at, a.gate + at, g) : S::load(a.gate, g, a.C), w);
+                words(token ? pipe.read(turn, gate_at, a.gate + at, g, C) : span.load_vector(a.gate, g, C), w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float2 u = unpack_bf16x2(y[i]);
@@ -285,7 +295,7 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
                     else dx[i] = pack_bf16x2(fmul2(dt[g][i], u));
                     dt[g][i] = fmul2(dt[g][i], unpack_bf16x2(w[i]));
                 }
-                if (token) S::store(a.dgate_token + at, g, a.C, dx);
+                if (token) span.store(a.dgate_token + at, g, C, dx);
             }
             if (post) {
 #pragma unroll
@@ -298,7 +308,7 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dx[i] = pack_bf16x2(dt[g][i]);
-                S::store(a.dy + at, g, a.C, dx);
+                span.store(a.dy + at, g, C, dx);
             }
         }
         if (!post) continue;
@@ -306,11 +316,11 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             uint32_t y[4];
-            words(pipe.read(turn, y_at, a.y + at, g), y);
+            words(pipe.read(turn, y_at, a.y + at, g, C), y);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 y[i] = pack_bf16x2(ffma2(fmul2(unpack_bf16x2(y[i]), ry), c2, fmul2(dt[g][i], ry)));
-            S::store(a.dy + at, g, a.C, y);
+            span.store(a.dy + at, g, C, y);
         }
     }
     const size_t slab = static_cast<size_t>(gridDim.x) * a.C;
@@ -330,12 +340,12 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
 #pragma unroll
             for (int k = 0; k < 3; ++k)
                 if (k < sums) {
-                    const int c0 = S::col(g, 2 * i), c1 = S::col(g, 2 * i + 1);
-                    if (VEC == 8) {      // c0 < C says the whole group is inside
-                        if (c0 < a.C) *reinterpret_cast<float2*>(p + k * slab + c0) = v[k];
+                    const int c = span.col(g, 2 * i);
+                    if (VEC == 8) {      // c < C says the whole group is inside
+                        if (c < a.C) *reinterpret_cast<float2*>(p + k * slab + c) = v[k];
                     } else {
-                        if (c0 < a.C) p[k * slab + c0] = v[k].x;
-                        if (c1 < a.C) p[k * slab + c1] = v[k].y;
+                        if (c >= 0 && c < a.C) p[k * slab + c] = v[k].x;
+                        if (c + 1 < a.C) p[k * slab + c + 1] = v[k].y;
                     }
                 }
         }

@@ -7,14 +7,14 @@ namespace {
 // Bytes of a two-stage row pipe.
 template <int T, int G, int VEC>
 size_t pipe_bytes(int arrays) {
-    return VEC == 8 ? static_cast<size_t>(2) * arrays * G * T * 16 : 0;
+    return static_cast<size_t>(2) * arrays * G * T * 16;
 }
 
 template <int T, int G, int VEC>
 struct NormLaunch {
     static w4_status run(const w4::NormArgs& a, int sms, cudaStream_t st) {
         const size_t smem = pipe_bytes<T, G, VEC>(1 + (a.y ? 1 : 0) + (a.gate_kind == w4::kGateToken ? 1 : 0));
-        const int grid = std::min(a.M, sms * (1024 / T));
+        const int grid = row_grid(a.M, sms * (1024 / T));
         auto fn = a.scales ? w4::block_norm_kernel<T, G, VEC, true> : w4::block_norm_kernel<T, G, VEC, false>;
         if (smem > 40 * 1024 && ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
         launch_pdl(fn, dim3(grid), dim3(T), smem, st, a);
@@ -26,7 +26,7 @@ struct NormLaunch {
 template <int T, int G, int VEC>
 struct NormGradBlocks {
     static int run(int M, int sms) {
-        return std::min(M, sms * w4::norm_grad_blocks_per_sm(T, G));
+        return row_grid(M, sms * w4::norm_grad_blocks_per_sm(T, G));
     }
 };
 int norm_grad_blocks(int M, int C, int sms) { return dispatch_row<NormGradBlocks>(C, M, sms); }

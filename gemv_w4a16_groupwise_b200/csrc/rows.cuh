@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "tma.cuh"
 
 namespace w4 {
 
@@ -23,17 +24,30 @@ __device__ __forceinline__ uint16_t to_bf16_bits(float v) { return __bfloat16_as
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // A thread's columns of a row: G groups of 8 values, held as 4 words of
-// bf16x2.  VEC = 8: a group is 8 consecutive columns, groups of the block's
-// threads side by side (rows of whole 16 bytes).  VEC = 1: its values lie T
-// columns apart, for the other widths.  Columns past C read as 0, which is
-// neutral in every sum and maximum here.
+// bf16x2.  Columns outside the row read as 0, which is neutral in every sum
+// and maximum here.
+//
+// VEC = 8: a group is 8 consecutive columns, groups of the block's threads
+// side by side (rows of whole 16 bytes).
+// VEC = 2: the other widths.  A word of a group is a whole word of memory, the
+// words of the block's threads side by side: in a row that starts at an odd
+// value (`shift` = 1) the pairs begin at column -1, whose half belongs to the
+// row before.  A block's rows lie an even number of rows apart, so `shift` is
+// the same for all of them and a thread keeps its columns.
 template <int T, int G, int VEC>
 struct RowSpan {
-    __device__ static __forceinline__ int col(int g, int i) {     // column of value i of group g
-        return VEC == 8 ? (g * T + static_cast<int>(threadIdx.x)) * 8 + i
-                        : (g * 8 + i) * T + static_cast<int>(threadIdx.x);
+    int shift;       // 1: the block's rows start in the middle of a word
+    int c0;          // first column of this piece of a row (0 but in long rows)
+
+    // the span of the rows of C values that start at m * C, m = first row's number
+    __device__ __forceinline__ explicit RowSpan(long long m, int C, int c0_ = 0)
+        : shift(VEC == 8 ? 0 : static_cast<int>(m & C & 1)), c0(c0_) {}
+    __device__ __forceinline__ int col(int g, int i) const {     // column of value i of group g
+        return c0 + (VEC == 8 ? (g * T + static_cast<int>(threadIdx.x)) * 8 + i
+                              : ((g * 4 + (i >> 1)) * T + static_cast<int>(threadIdx.x)) * 2 + (i & 1) - shift);
     }
-    __device__ static __forceinline__ uint4 load(const uint16_t* row, int g, int C) {
+    // a row of the matrix
+    __device__ __forceinline__ uint4 load(const uint16_t* row, int g, int C) const {
         if constexpr (VEC == 8) {
             const int c = col(g, 0);
             return c < C ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -41,22 +55,37 @@ struct RowSpan {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int c0 = col(g, 2 * i), c1 = col(g, 2 * i + 1);
-                w[i] = (c0 < C ? row[c0] : 0u) | ((c1 < C ? static_cast<uint32_t>(row[c1]) : 0u) << 16);
+                const int c = col(g, 2 * i);
+                w[i] = 0u;
+                if (c >= 0 && c + 1 < C) w[i] = *reinterpret_cast<const uint32_t*>(row + c);
+                else if (c >= 0 && c < C) w[i] = row[c];
+                else if (c == -1 && C > 0) w[i] = static_cast<uint32_t>(row[0]) << 16;
             }
             return make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    __device__ static __forceinline__ void store(uint16_t* row, int g, int C, const uint32_t (&w)[4]) {
+    // a vector over the columns (its words are not the matrix's when shift = 1)
+    __device__ __forceinline__ uint4 load_vector(const uint16_t* v, int g, int C) const {
+        if (VEC == 8 || shift == 0) return load(v, g, C);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = col(g, 2 * i);
+            w[i] = (c >= 0 && c < C ? v[c] : 0u) | (c + 1 < C ? static_cast<uint32_t>(v[c + 1]) << 16 : 0u);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void store(uint16_t* row, int g, int C, const uint32_t (&w)[4]) const {
         if constexpr (VEC == 8) {
             const int c = col(g, 0);
             if (c < C) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int c0 = col(g, 2 * i), c1 = col(g, 2 * i + 1);
-                if (c0 < C) row[c0] = static_cast<uint16_t>(w[i]);
-                if (c1 < C) row[c1] = static_cast<uint16_t>(w[i] >> 16);
+                const int c = col(g, 2 * i);
+                if (c >= 0 && c + 1 < C) *reinterpret_cast<uint32_t*>(row + c) = w[i];
+                else if (c >= 0 && c < C) row[c] = static_cast<uint16_t>(w[i]);
+                else if (c == -1 && C > 0) row[0] = static_cast<uint16_t>(w[i] >> 16);
             }
         }
     }
@@ -70,15 +99,28 @@ struct RowSpan {
 template <int T, int G, int VEC, bool PIPED>
 struct RowPipe {
     using S = RowSpan<T, G, VEC>;
-    uint4* base;             // [2][arrays][G * T]
-    int arrays, C;
-    __device__ __forceinline__ void fetch(int stage, int array, const uint16_t* row) const {
-        if constexpr (PIPED) {
+    uint4* base;             // [2][arrays][G * T], or as many words [G * 4][T]
+    int arrays;
+    S span;
+    __device__ __forceinline__ uint32_t* words(int stage, int array, int g) const {
+        return reinterpret_cast<uint32_t*>(base + (stage * arrays + array) * (G * T)) + g * 4 * T + threadIdx.x;
+    }
+    __device__ __forceinline__ void fetch(int stage, int array, const uint16_t* row, int C) const {
+        if constexpr (!PIPED) return;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int c = S::col(g, 0);
+        for (int g = 0; g < G; ++g) {
+            if constexpr (VEC == 8) {
+                const int c = span.col(g, 0);
                 cp_async_16_zfill(base + (stage * arrays + array) * (G * T) + g * T + threadIdx.x,
                                   row + (c < C ? c : 0), c < C);
+            } else {
+                // a word's bytes inside the row, but for the half at column -1 (read() drops it)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = span.col(g, 2 * i);
+                    cp_async_4(words(stage, array, g) + i * T, row + (c < C ? c : -span.shift),
+                               c + 1 < C ? 4u : c < C ? 2u : 0u);
+                }
             }
         }
     }
@@ -92,11 +134,23 @@ struct RowPipe {
             else asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
     }
-    __device__ __forceinline__ uint4 read(int stage, int array, const uint16_t* row, int g) const {
-        if constexpr (PIPED) return base[(stage * arrays + array) * (G * T) + g * T + threadIdx.x];
-        else return S::load(row, g, C);
+    __device__ __forceinline__ uint4 read(int stage, int array, const uint16_t* row, int g, int C) const {
+        if constexpr (!PIPED) return span.load(row, g, C);
+        if constexpr (VEC == 8) return base[(stage * arrays + array) * (G * T) + g * T + threadIdx.x];
+        const uint32_t* w = words(stage, array, g);
+        uint4 v = make_uint4(w[0], w[T], w[2 * T], w[3 * T]);
+        if (g == 0 && threadIdx.x == 0 && span.shift) v.x &= 0xFFFF0000u;
+        return v;
     }
 };
+
+// The row length, as a value that the compiler takes for new: without it the
+// columns' comparisons are all hoisted out of a kernel's loop over rows and
+// spilled.
+__device__ __forceinline__ int fresh(int C) {
+    asm volatile("" : "+r"(C));
+    return C;
+}
 
 // Sum over the block's T threads in a fixed order, in every thread.  One
 // barrier; `buf` (32 entries, 16-byte aligned) is not written again before another barrier has passed.

@@ -19,19 +19,22 @@ w4_status check_w8(int M, int N, int K, long long ldw, int transposed, const voi
 template <template <int, int, int> class Launch, typename... Args>
 auto dispatch_row(int C, Args... args) {
     const bool vec = C % 8 == 0;
-    if (C <= 1024) return vec ? Launch<128, 1, 8>::run(args...) : Launch<128, 1, 1>::run(args...);
-    if (C <= 2048) return vec ? Launch<256, 1, 8>::run(args...) : Launch<256, 1, 1>::run(args...);
-    if (C <= 4096) return vec ? Launch<256, 2, 8>::run(args...) : Launch<256, 2, 1>::run(args...);
-    if (C <= 8192) return vec ? Launch<512, 2, 8>::run(args...) : Launch<512, 2, 1>::run(args...);
-    return vec ? Launch<1024, 2, 8>::run(args...) : Launch<1024, 2, 1>::run(args...);
+    if (C <= 1024) return vec ? Launch<128, 1, 8>::run(args...) : Launch<128, 1, 2>::run(args...);
+    if (C <= 2048) return vec ? Launch<256, 1, 8>::run(args...) : Launch<256, 1, 2>::run(args...);
+    if (C <= 4096) return vec ? Launch<256, 2, 8>::run(args...) : Launch<256, 2, 2>::run(args...);
+    if (C <= 8192) return vec ? Launch<512, 2, 8>::run(args...) : Launch<512, 2, 2>::run(args...);
+    return vec ? Launch<1024, 2, 8>::run(args...) : Launch<1024, 2, 2>::run(args...);
 }
+
+// Blocks that walk over M rows: a row each, or an even number (see RowSpan).
+int row_grid(int M, int blocks) { return M <= blocks ? M : std::max(2, blocks & ~1); }
 
 template <int T, int G, int VEC>
 struct QuantizeLaunch {
     static w4_status run(const uint16_t* X, int R, int C, const float* channel, int8_t* codes, long long ld,
                          float* scales, int sms, cudaStream_t st) {
         auto fn = channel ? w4::quantize_rows_kernel<T, G, VEC, true> : w4::quantize_rows_kernel<T, G, VEC, false>;
-        launch_pdl(fn, dim3(std::min(R, sms * (1024 / T))), dim3(T), 0, st, X, R, C, channel, codes, ld, scales);
+        launch_pdl(fn, dim3(row_grid(R, sms * (1024 / T))), dim3(T), 0, st, X, R, C, channel, codes, ld, scales);
         return launch_status();
     }
 };
@@ -47,7 +50,7 @@ w4_status run_quantize_rows(const uint16_t* X, int R, int C, const float* channe
     if (C % 8 == 0)
         launch_pdl(w4::quantize_long_rows_kernel<8>, dim3(R), dim3(1024), 0, st, X, C, channel, codes, ld, scales);
     else
-        launch_pdl(w4::quantize_long_rows_kernel<1>, dim3(R), dim3(1024), 0, st, X, C, channel, codes, ld, scales);
+        launch_pdl(w4::quantize_long_rows_kernel<2>, dim3(R), dim3(1024), 0, st, X, C, channel, codes, ld, scales);
     return launch_status();
 }
 

@@ -76,30 +76,36 @@ __device__ __forceinline__ uint2 codes8(float2 (&v)[4], const RowCodes& s) {
 }
 
 // The codes of a thread's group to its row.
-template <class S, int VEC>
-__device__ __forceinline__ void store_codes(int8_t* row, int g, int C, uint2 w) {
+template <int VEC, class S>
+__device__ __forceinline__ void store_codes(const S& span, int8_t* row, int g, int C, uint2 w) {
     if constexpr (VEC == 8) {
-        const int c = S::col(g, 0);
+        const int c = span.col(g, 0);
         if (c < C) *reinterpret_cast<uint2*>(row + c) = w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = S::col(g, i);
-            if (c < C) row[c] = static_cast<int8_t>((i < 4 ? w.x >> (8 * i) : w.y >> (8 * (i - 4))) & 0xFFu);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t pair = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
+            const int c = span.col(g, 2 * i);
+            if (span.shift == 0 && c + 1 < C) {
+                *reinterpret_cast<uint16_t*>(row + c) = static_cast<uint16_t>(pair);
+            } else {
+                if (c >= 0 && c < C) row[c] = static_cast<int8_t>(pair & 0xFFu);
+                if (c + 1 < C) row[c + 1] = static_cast<int8_t>((pair >> 8) & 0xFFu);
+            }
         }
     }
 }
 
 // A group's values times their channel factors.
-template <class S, int VEC>
-__device__ __forceinline__ void channel_values(float2 (&v)[4], uint4 x, const float* __restrict__ channel, int g,
-                                               int C) {
+template <int VEC, class S>
+__device__ __forceinline__ void channel_values(const S& span, float2 (&v)[4], uint4 x,
+                                               const float* __restrict__ channel, int g, int C) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = unpack_bf16x2(w[i]);
     if (channel == nullptr) return;
     if constexpr (VEC == 8) {
-        const int c = S::col(g, 0);
+        const int c = span.col(g, 0);
         if (c < C) {
             const float4 lo = __ldg(reinterpret_cast<const float4*>(channel + c));
             const float4 hi = __ldg(reinterpret_cast<const float4*>(channel + c + 4));
@@ -111,8 +117,15 @@ __device__ __forceinline__ void channel_values(float2 (&v)[4], uint4 x, const fl
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c0 = S::col(g, 2 * i), c1 = S::col(g, 2 * i + 1);
-            v[i] = fmul2(v[i], make_float2(c0 < C ? __ldg(channel + c0) : 0.0f, c1 < C ? __ldg(channel + c1) : 0.0f));
+            const int c = span.col(g, 2 * i);
+            float2 f = both(0.0f);
+            if (span.shift == 0 && c + 1 < C) {
+                f = __ldg(reinterpret_cast<const float2*>(channel + c));
+            } else {
+                if (c >= 0 && c < C) f.x = __ldg(channel + c);
+                if (c + 1 < C) f.y = __ldg(channel + c + 1);
+            }
+            v[i] = fmul2(v[i], f);
         }
     }
 }
@@ -126,20 +139,21 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
                                                                     const float* __restrict__ channel,
                                                                     int8_t* __restrict__ codes, long long ld,
                                                                     float* __restrict__ scales) {
-    using S = RowSpan<T, G, VEC>;
+    const RowSpan<T, G, VEC> span(blockIdx.x, C);
     __shared__ __align__(16) uint32_t buf[2][32];
     pdl_wait();
     pdl_launch_dependents();
     uint4 x[G], next[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) next[g] = S::load(X + static_cast<size_t>(blockIdx.x) * C, g, C);
+    for (int g = 0; g < G; ++g) next[g] = span.load(X + static_cast<size_t>(blockIdx.x) * C, g, C);
     int turn = 0;
     for (long long m = blockIdx.x; m < R; m += gridDim.x, turn ^= 1) {
         const bool more = m + gridDim.x < R;
+        if (VEC != 8) C = fresh(C);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             x[g] = next[g];
-            if (more) next[g] = S::load(X + static_cast<size_t>(m + gridDim.x) * C, g, C);
+            if (more) next[g] = span.load(X + static_cast<size_t>(m + gridDim.x) * C, g, C);
         }
         uint32_t top;
         float2 v[CHANNEL ? G : 1][4];       // products with the factors are kept, plain values unpacked again
@@ -147,7 +161,7 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
             float t = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                channel_values<S, VEC>(v[g], x[g], channel, g, C);
+                channel_values<VEC>(span, v[g], x[g], channel, g, C);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t = max_abs(t, v[g][i]);
             }
@@ -165,8 +179,8 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float2(&u)[4] = v[CHANNEL ? g : 0];
-            if constexpr (!CHANNEL) channel_values<S, VEC>(u, x[g], nullptr, g, C);
-            store_codes<S, VEC>(codes + static_cast<size_t>(m) * ld, g, C, codes8(u, sc));
+            if constexpr (!CHANNEL) channel_values<VEC>(span, u, x[g], nullptr, g, C);
+            store_codes<VEC>(span, codes + static_cast<size_t>(m) * ld, g, C, codes8(u, sc));
         }
     }
 }
@@ -178,7 +192,6 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
                                                                   const float* __restrict__ channel,
                                                                   int8_t* __restrict__ codes, long long ld,
                                                                   float* __restrict__ scales) {
-    using S = RowSpan<1024, 1, VEC>;
     __shared__ __align__(16) uint32_t buf[32];
     const size_t m = blockIdx.x;
     const uint16_t* x = X + m * C;
@@ -186,9 +199,10 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
     pdl_launch_dependents();
     float t = 0.0f;
 #pragma unroll 2
-    for (int c = 0; c < C; c += 8192) {
+    for (int c0 = 0; c0 <= C; c0 += 8192) {       // a shifted row's last value may be in a piece of its own
+        const RowSpan<1024, 1, VEC> span(m, C, c0);
         float2 v[4];
-        channel_values<S, VEC>(v, S::load(x + c, 0, C - c), channel ? channel + c : nullptr, 0, C - c);
+        channel_values<VEC>(span, v, span.load(x, 0, C), channel, 0, C);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t = max_abs(t, v[i]);
     }
@@ -196,10 +210,11 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
     const RowCodes sc = row_codes(t);
     if (threadIdx.x == 0) scales[m] = row_scale(t);
 #pragma unroll 2
-    for (int c = 0; c < C; c += 8192) {
+    for (int c0 = 0; c0 <= C; c0 += 8192) {
+        const RowSpan<1024, 1, VEC> span(m, C, c0);
         float2 v[4];
-        channel_values<S, VEC>(v, S::load(x + c, 0, C - c), channel ? channel + c : nullptr, 0, C - c);
-        store_codes<S, VEC>(codes + m * ld + c, 0, C - c, codes8(v, sc));
+        channel_values<VEC>(span, v, span.load(x, 0, C), channel, 0, C);
+        store_codes<VEC>(span, codes + m * ld, 0, C, codes8(v, sc));
     }
 }
 
