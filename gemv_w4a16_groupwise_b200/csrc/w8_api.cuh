@@ -34,7 +34,9 @@ struct QuantizeLaunch {
     static w4_status run(const uint16_t* X, int R, int C, const float* channel, int8_t* codes, long long ld,
                          float* scales, int sms, cudaStream_t st) {
         auto fn = channel ? w4::quantize_rows_kernel<T, G, VEC, true> : w4::quantize_rows_kernel<T, G, VEC, false>;
-        launch_pdl(fn, dim3(row_grid(R, sms * (1024 / T))), dim3(T), 0, st, X, R, C, channel, codes, ld, scales);
+        const size_t smem = channel ? static_cast<size_t>(G) * T * 32 : 0;
+        if (smem > 40 * 1024 && ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
+        launch_pdl(fn, dim3(row_grid(R, sms * (1024 / T))), dim3(T), smem, st, X, R, C, channel, codes, ld, scales);
         return launch_status();
     }
 };

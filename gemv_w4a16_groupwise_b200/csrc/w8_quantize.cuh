@@ -96,56 +96,67 @@ __device__ __forceinline__ void store_codes(const S& span, int8_t* row, int g, i
     }
 }
 
-// A group's values times their channel factors.
+// A group's channel factors from memory.
 template <int VEC, class S>
-__device__ __forceinline__ void channel_values(const S& span, float2 (&v)[4], uint4 x,
-                                               const float* __restrict__ channel, int g, int C) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ void channel_factors(const S& span, float2 (&f)[4], const float* __restrict__ channel, int g,
+                                                int C) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = unpack_bf16x2(w[i]);
-    if (channel == nullptr) return;
+    for (int i = 0; i < 4; ++i) f[i] = both(0.0f);
     if constexpr (VEC == 8) {
         const int c = span.col(g, 0);
         if (c < C) {
             const float4 lo = __ldg(reinterpret_cast<const float4*>(channel + c));
             const float4 hi = __ldg(reinterpret_cast<const float4*>(channel + c + 4));
-            v[0] = fmul2(v[0], make_float2(lo.x, lo.y));
-            v[1] = fmul2(v[1], make_float2(lo.z, lo.w));
-            v[2] = fmul2(v[2], make_float2(hi.x, hi.y));
-            v[3] = fmul2(v[3], make_float2(hi.z, hi.w));
+            f[0] = make_float2(lo.x, lo.y);
+            f[1] = make_float2(lo.z, lo.w);
+            f[2] = make_float2(hi.x, hi.y);
+            f[3] = make_float2(hi.z, hi.w);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = span.col(g, 2 * i);
-            float2 f = both(0.0f);
-            if (span.shift == 0 && c + 1 < C) {
-                f = __ldg(reinterpret_cast<const float2*>(channel + c));
-            } else {
-                if (c >= 0 && c < C) f.x = __ldg(channel + c);
-                if (c + 1 < C) f.y = __ldg(channel + c + 1);
-            }
-            v[i] = fmul2(v[i], f);
+            if (c >= 0 && c < C) f[i].x = __ldg(channel + c);
+            if (c + 1 < C) f[i].y = __ldg(channel + c + 1);
         }
     }
 }
 
+__device__ __forceinline__ void unpack8(float2 (&v)[4], uint4 x) {
+    v[0] = unpack_bf16x2(x.x);
+    v[1] = unpack_bf16x2(x.y);
+    v[2] = unpack_bf16x2(x.z);
+    v[3] = unpack_bf16x2(x.w);
+}
+
 // Rows of at most 16384: a block holds a row in registers between the maximum
 // and the codes, so the row is read once, and has the next row's loads under
-// way meanwhile.  Bound by device memory (3 bytes an element).  The channel
-// factors (twice a row's bytes) come from L1, once a row.
+// way meanwhile.  Bound by device memory (3 bytes an element).  Every thread
+// keeps the channel factors of its columns (twice a row's bytes) in shared
+// memory, 16 bytes of a thread beside its neighbours': from L1, 32 bytes apart,
+// they took most of the time of a row.
 template <int T, int G, int VEC, bool CHANNEL>
-__global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
+__global__ void __launch_bounds__(T, CHANNEL && G > 2 ? 1 : 1024 / T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
                                                                     const float* __restrict__ channel,
                                                                     int8_t* __restrict__ codes, long long ld,
                                                                     float* __restrict__ scales) {
     const RowSpan<T, G, VEC> span(blockIdx.x, C);
+    extern __shared__ float4 factors[];      // CHANNEL: [2 G][T]
     __shared__ __align__(16) uint32_t buf[2][32];
     pdl_wait();
     pdl_launch_dependents();
     uint4 x[G], next[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) next[g] = span.load(X + static_cast<size_t>(blockIdx.x) * C, g, C);
+    if constexpr (CHANNEL) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float2 f[4];
+            channel_factors<VEC>(span, f, channel, g, C);
+            factors[2 * g * T + threadIdx.x] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+            factors[(2 * g + 1) * T + threadIdx.x] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        }
+    }
     int turn = 0;
     for (long long m = blockIdx.x; m < R; m += gridDim.x, turn ^= 1) {
         const bool more = m + gridDim.x < R;
@@ -161,7 +172,12 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
             float t = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                channel_values<VEC>(span, v[g], x[g], channel, g, C);
+                const float4 lo = factors[2 * g * T + threadIdx.x], hi = factors[(2 * g + 1) * T + threadIdx.x];
+                unpack8(v[g], x[g]);
+                v[g][0] = fmul2(v[g][0], make_float2(lo.x, lo.y));
+                v[g][1] = fmul2(v[g][1], make_float2(lo.z, lo.w));
+                v[g][2] = fmul2(v[g][2], make_float2(hi.x, hi.y));
+                v[g][3] = fmul2(v[g][3], make_float2(hi.z, hi.w));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t = max_abs(t, v[g][i]);
             }
@@ -179,7 +195,7 @@ __global__ void __launch_bounds__(T, 1024 / T) quantize_rows_kernel(const uint16
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float2(&u)[4] = v[CHANNEL ? g : 0];
-            if constexpr (!CHANNEL) channel_values<VEC>(span, u, x[g], nullptr, g, C);
+            if constexpr (!CHANNEL) unpack8(u, x[g]);
             store_codes<VEC>(span, codes + static_cast<size_t>(m) * ld, g, C, codes8(u, sc));
         }
     }
@@ -197,12 +213,21 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
     const uint16_t* x = X + m * C;
     pdl_wait();
     pdl_launch_dependents();
+    auto values = [&](const RowSpan<1024, 1, VEC>& span, float2 (&v)[4]) {
+        unpack8(v, span.load(x, 0, C));
+        if (channel) {
+            float2 f[4];
+            channel_factors<VEC>(span, f, channel, 0, C);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = fmul2(v[i], f[i]);
+        }
+    };
     float t = 0.0f;
 #pragma unroll 2
     for (int c0 = 0; c0 <= C; c0 += 8192) {       // a shifted row's last value may be in a piece of its own
         const RowSpan<1024, 1, VEC> span(m, C, c0);
         float2 v[4];
-        channel_values<VEC>(span, v, span.load(x, 0, C), channel, 0, C);
+        values(span, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t = max_abs(t, v[i]);
     }
@@ -213,7 +238,7 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
     for (int c0 = 0; c0 <= C; c0 += 8192) {
         const RowSpan<1024, 1, VEC> span(m, C, c0);
         float2 v[4];
-        channel_values<VEC>(span, v, span.load(x, 0, C), channel, 0, C);
+        values(span, v);
         store_codes<VEC>(span, codes + m * ld, 0, C, codes8(v, sc));
     }
 }
