@@ -66,14 +66,18 @@ struct RowSpan {
     }
     // a vector over the columns (its words are not the matrix's when shift = 1)
     __device__ __forceinline__ uint4 load_vector(const uint16_t* v, int g, int C) const {
-        if (VEC == 8 || shift == 0) return load(v, g, C);
-        uint32_t w[4];
+        if constexpr (VEC == 8) {
+            return load(v, g, C);
+        } else {
+            if (shift == 0) return load(v, g, C);
+            uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = col(g, 2 * i);
-            w[i] = (c >= 0 && c < C ? v[c] : 0u) | (c + 1 < C ? static_cast<uint32_t>(v[c + 1]) << 16 : 0u);
+            for (int i = 0; i < 4; ++i) {
+                const int c = col(g, 2 * i);
+                w[i] = (c >= 0 && c < C ? v[c] : 0u) | (c + 1 < C ? static_cast<uint32_t>(v[c + 1]) << 16 : 0u);
+            }
+            return make_uint4(w[0], w[1], w[2], w[3]);
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ void store(uint16_t* row, int g, int C, const uint32_t (&w)[4]) const {
         if constexpr (VEC == 8) {
@@ -106,9 +110,8 @@ struct RowPipe {
         return reinterpret_cast<uint32_t*>(base + (stage * arrays + array) * (G * T)) + g * 4 * T + threadIdx.x;
     }
     __device__ __forceinline__ void fetch(int stage, int array, const uint16_t* row, int C) const {
-        if constexpr (!PIPED) return;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+        for (int g = 0; PIPED && g < G; ++g) {
             if constexpr (VEC == 8) {
                 const int c = span.col(g, 0);
                 cp_async_16_zfill(base + (stage * arrays + array) * (G * T) + g * T + threadIdx.x,
@@ -135,12 +138,16 @@ struct RowPipe {
         }
     }
     __device__ __forceinline__ uint4 read(int stage, int array, const uint16_t* row, int g, int C) const {
-        if constexpr (!PIPED) return span.load(row, g, C);
-        if constexpr (VEC == 8) return base[(stage * arrays + array) * (G * T) + g * T + threadIdx.x];
-        const uint32_t* w = words(stage, array, g);
-        uint4 v = make_uint4(w[0], w[T], w[2 * T], w[3 * T]);
-        if (g == 0 && threadIdx.x == 0 && span.shift) v.x &= 0xFFFF0000u;
-        return v;
+        if constexpr (!PIPED) {
+            return span.load(row, g, C);
+        } else if constexpr (VEC == 8) {
+            return base[(stage * arrays + array) * (G * T) + g * T + threadIdx.x];
+        } else {
+            const uint32_t* w = words(stage, array, g);
+            uint4 v = make_uint4(w[0], w[T], w[2 * T], w[3 * T]);
+            if (g == 0 && threadIdx.x == 0 && span.shift) v.x &= 0xFFFF0000u;
+            return v;
+        }
     }
 };
 

@@ -36,10 +36,14 @@ constexpr int kW8ABytes = 128 * kW8Red;
 constexpr int kW8EpiWarps = 8;
 constexpr int kW8Threads = 64 + 32 * kW8EpiWarps;
 // An epilogue warp stages 32 outputs of 16 token pairs, the pairs 36 words
-// apart (two pairs' 16-byte reads then meet no bank twice), and 32 scales.
+// apart (two pairs' 16-byte reads then meet no bank twice), and its tokens' scales.
+// Where rows of Y are not whole 16 bytes, four warps stage 128 outputs of 32
+// tokens together instead, the tokens 272 bytes apart (17 x 16).
 constexpr int kW8PairStride = 36;
-constexpr int kW8EpiWarpBytes = 16 * kW8PairStride * 4 + 32 * 4;
+constexpr int kW8EpiWarpBytes = 16 * kW8PairStride * 4 + 128 * 4;
 constexpr int kW8EpiBytes = kW8EpiWarps * kW8EpiWarpBytes;
+constexpr int kW8TokenStride = 136;
+static_assert(32 * kW8TokenStride * 2 <= 4 * 16 * kW8PairStride * 4, "staging");
 
 __host__ __device__ constexpr int w8_stage_bytes(int TN) { return kW8ABytes + TN / 2 * kW8Red; }
 
@@ -116,6 +120,17 @@ __device__ __forceinline__ void umma_commit_pair_elected(uint32_t bar) {
         " @P tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
             bar)
         : "memory");
+}
+// Whether `yes` holds in all `count` threads that meet at barrier `id`.
+__device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t count, bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"(count), "r"(yes ? 1u : 0u)
+        : "memory");
+    return r != 0;
 }
 // mbar_wait_bounded by a whole warp, with one answer.
 __device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
@@ -330,8 +345,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         const int half = (warp - 2) >> 2;
         constexpr int kBlocks = TN >= 64 ? TN / 64 : 1;
         const int cbase = half * kBlocks * 32;  // TN = 32: the second half has nothing
-        uint32_t* stage = reinterpret_cast<uint32_t*>(epi + (warp - 2) * kW8EpiWarpBytes);
-        float* scales = reinterpret_cast<float*>(stage + 16 * kW8PairStride);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(epi) + (warp - 2) * 16 * kW8PairStride;
+        uint16_t* stage4 = reinterpret_cast<uint16_t*>(epi + half * 4 * 16 * kW8PairStride * 4);
+        float* scales = reinterpret_cast<float*>(epi + kW8EpiWarps * 16 * kW8PairStride * 4) + (warp - 2) * 128;
+        const bool whole16 = (out & 7) == 0;
         int i = 0;
         pdl_wait();
         while (walk.next(&u)) {
@@ -345,19 +362,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
             const float ws = (!TR && ov) ? a.p.w_scales[o] : 1.0f;
             const float bias = (a.p.bias && ov) ? bf16_bits_to_float(a.p.bias[o]) : 0.0f;
             const int tokens = cbase < TN ? min(kBlocks * 32, a.p.M - m0) : 0;
-            float as[kBlocks];
+            __syncwarp();
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                as[b] = 32 * b + lane < tokens ? a.p.a_scales[m0 + 32 * b + lane] : 0.0f;
+                scales[32 * b + lane] = 32 * b + lane < tokens ? a.p.a_scales[m0 + 32 * b + lane] : 0.0f;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, abort_flag,
                                                                       kErrTimeoutAccum));
-            if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) break;
+            bool go = !__any_sync(0xFFFFFFFFu, !ok || *abort_flag);
+            // four warps that will meet at barriers go on, or give up, together
+            if (!whole16) go = named_barrier_and(1 + half, 128, go);
+            if (!go) break;
             tc_fence_after();
             const uint32_t acc =
                 tmem_d + static_cast<uint32_t>(buf * TN + cbase) + (static_cast<uint32_t>(32 * q) << 16);
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                if (32 * b >= tokens) break;
+            // not unrolled: straight-line code for every block of a tile was several
+            // microseconds of instruction fetches in each launch
+#pragma unroll 1
+            for (int b = 0; 32 * b < tokens; ++b) {
                 uint32_t r[32];
                 __syncwarp();
                 tmem_ld_x32(acc + static_cast<uint32_t>(32 * b), r);
@@ -367,13 +388,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
                     for (int e = 0; e < 32; ++e) pt[e * kW8Rows] = static_cast<int32_t>(r[e]);
                     continue;
                 }
-                scales[lane] = as[b];
-                __syncwarp();
                 // pairs of tokens as bf16x2
                 uint32_t y[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float2 sc = *reinterpret_cast<const float2*>(scales + 2 * e);
+                    const float2 sc = *reinterpret_cast<const float2*>(scales + 32 * b + 2 * e);
                     y[e] = bf162_bits(__floats2bfloat162_rn(
                         fmaf(static_cast<float>(static_cast<int>(r[2 * e])), sc.x * ws, bias),
                         fmaf(static_cast<float>(static_cast<int>(r[2 * e + 1])), sc.y * ws, bias)));
@@ -402,13 +421,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
                                            prmt(v1.x, v1.y, 0x7632u), prmt(v1.z, v1.w, 0x7632u));
                     }
                 } else {
-                    uint16_t* dst = a.p.Y + static_cast<size_t>(mb) * out + o;
+                    // rows of Y start anywhere: four warps put 128 outputs of the 32 tokens together and
+                    // store the whole 16 bytes among them as such (2 bytes a lane cost 10 cycles a store)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        if (ov && mb + 2 * e < a.p.M) dst[static_cast<size_t>(2 * e) * out] = static_cast<uint16_t>(y[e]);
-                        if (ov && mb + 2 * e + 1 < a.p.M)
-                            dst[static_cast<size_t>(2 * e + 1) * out] = static_cast<uint16_t>(y[e] >> 16);
+                        stage4[2 * e * kW8TokenStride + 32 * q + lane] = static_cast<uint16_t>(y[e]);
+                        stage4[(2 * e + 1) * kW8TokenStride + 32 * q + lane] = static_cast<uint16_t>(y[e] >> 16);
                     }
+                    named_barrier_sync(1 + half, 128);
+                    const int oc = o0 + static_cast<int>(rank) * 128;      // first output of the CTA's rows
+                    const int valid = min(128, out - oc), live = min(32, tokens - 32 * b);
+                    // 16 chunks, and 16 single outputs around them, of 8 tokens at a time
+                    const int sub = (32 * q + lane) >> 4, j = lane & 15;
+                    for (int tok = sub; tok < live; tok += 8) {
+                        const size_t row0 = static_cast<size_t>(mb + tok) * out + oc;
+                        const uint16_t* src = stage4 + tok * kW8TokenStride;
+                        const int head = static_cast<int>(-static_cast<int>(row0 & 7) & 7);   // outputs before the chunks
+                        const int e0 = head + 8 * j;
+                        if (e0 + 8 <= valid) {
+                            const uint32_t* w = reinterpret_cast<const uint32_t*>(src + (e0 & ~1));
+                            const uint32_t sh = (e0 & 1) * 16;
+                            uint32_t v[5];
+#pragma unroll
+                            for (int k = 0; k < 5; ++k) v[k] = w[k];
+                            *reinterpret_cast<uint4*>(a.p.Y + row0 + e0) =
+                                make_uint4(__funnelshift_r(v[0], v[1], sh), __funnelshift_r(v[1], v[2], sh),
+                                           __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
+                        }
+                        const int chunks = valid > head ? (valid - head) >> 3 : 0;
+                        const int single = j < 8 ? j : head + 8 * chunks + j - 8;
+                        if (j < 8 ? j < min(head, valid) : single < valid && single >= head) a.p.Y[row0 + single] = src[single];
+                    }
+                    named_barrier_sync(1 + half, 128);
                 }
             }
             // this warp's reads of the buffer are complete
