@@ -137,7 +137,9 @@ w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, bool
         return W4_ERR_CUDA;
     auto fn = w4::w8_gemm_tc_kernel<TR, TN>;
     if (ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
-    const w4::W8TcArgs a = {g, part, p.tiles_m, p.tiles, p.F, p.chunks, p.cut_pairs, stages, early ? 1 : 0};
+    const w4::W8TcArgs a = {g, part, p.tiles_m, p.tiles, static_cast<uint32_t>((1ull << 32) / p.tiles_m + 1),
+                            p.grid_pairs % p.tiles_m, p.grid_pairs / p.tiles_m, p.F, p.chunks, p.cut_pairs, stages,
+                            early ? 1 : 0};
     launch_pdl(fn, dim3(2 * p.grid_pairs), dim3(w4::kW8Threads), smem, st, wmap, amap, a);
     const w4_status s = launch_status();
     if (s != W4_OK || p.ws == 0) return s;

@@ -37,20 +37,17 @@ constexpr int kW8EpiWarps = 8;
 constexpr int kW8Threads = 64 + 32 * kW8EpiWarps;
 // An epilogue warp stages 32 outputs of 16 token pairs, the pairs 36 words
 // apart (two pairs' 16-byte reads then meet no bank twice), and its tokens' scales.
-// Where rows of Y are not whole 16 bytes, four warps stage 128 outputs of 32
-// tokens together instead, the tokens 272 bytes apart (17 x 16).
 constexpr int kW8PairStride = 36;
 constexpr int kW8EpiWarpBytes = 16 * kW8PairStride * 4 + 128 * 4;
 constexpr int kW8EpiBytes = kW8EpiWarps * kW8EpiWarpBytes;
-constexpr int kW8TokenStride = 136;
-static_assert(32 * kW8TokenStride * 2 <= 4 * 16 * kW8PairStride * 4, "staging");
-
 __host__ __device__ constexpr int w8_stage_bytes(int TN) { return kW8ABytes + TN / 2 * kW8Red; }
 
 struct W8TcArgs {
     W8Args p;
     int32_t* part;       // [2 pairs][TN][256] partial tiles
-    int tiles_m, tiles;  // token tiles, tiles in all
+    int tiles_m, tiles;  // token tiles, tiles in all (token tiles fastest)
+    uint32_t inv_tiles_m;     // floor(2^32 / tiles_m) + 1 (tiles_m > 1): exact quotients of pair numbers
+    int step_m, step_o;  // from a tile to the one `pairs` on
     int F;               // tiles below F are whole units
     int chunks;          // stages of one tile
     int cut_pairs;       // pairs that share the tiles from F on
@@ -121,17 +118,6 @@ __device__ __forceinline__ void umma_commit_pair_elected(uint32_t bar) {
             bar)
         : "memory");
 }
-// Whether `yes` holds in all `count` threads that meet at barrier `id`.
-__device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t count, bool yes) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n"
-        " selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"(id), "r"(count), "r"(yes ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
 // mbar_wait_bounded by a whole warp, with one answer.
 __device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                   unsigned int err) {
@@ -163,39 +149,50 @@ __host__ __device__ constexpr uint32_t umma_idesc_i8(int TN, bool a_mn_major) {
            | (static_cast<uint32_t>(kW8Rows >> 4) << 24);
 }
 
-// The units of pair p of P, in order.
+// The units of pair p of P, in order.  The walk is kept to a few instructions
+// (no division on the way to the first unit): every SM fetches a launch's code
+// afresh, all at once, and what stands before the first copies and scales is
+// paid in full.
 struct W8Unit {
-    int tile, kb0, kb1;
+    int mt, ot;          // token tile, output tile
+    int kb0, kb1;        // its stages
     int part;            // slot of the partial tile, or -1 for a whole tile
 };
 struct W8Walk {
-    int p, P, F, chunks;
-    int next_whole;
+    int t, mt, ot;       // the next whole tile
     uint32_t c, c1;      // the pair's share of the cut tiles' stages (< 2^10 pairs x 2^10 stages, squared at most 2^31)
     int cut_units;
-    __device__ W8Walk(const W8TcArgs& a, int pair, int pairs) {
-        p = pair;
-        P = pairs;
-        F = a.F;
-        chunks = a.chunks;
-        next_whole = pair;
-        const uint32_t total = pair < a.cut_pairs ? static_cast<uint32_t>(a.tiles - a.F) * a.chunks : 0u;
-        c = total * pair / a.cut_pairs;
-        c1 = total * (pair + 1) / a.cut_pairs;
+    __device__ __forceinline__ W8Walk(const W8TcArgs& a, int pair) {
+        t = pair;
+        ot = a.tiles_m == 1 ? pair : static_cast<int>(__umulhi(pair, a.inv_tiles_m));
+        mt = pair - ot * a.tiles_m;
+        c = c1 = 0;
         cut_units = 0;
+        if (a.F < a.tiles && pair < a.cut_pairs) {
+            const uint32_t total = static_cast<uint32_t>(a.tiles - a.F) * a.chunks;
+            c = total * pair / a.cut_pairs;
+            c1 = total * (pair + 1) / a.cut_pairs;
+        }
     }
-    __device__ bool next(W8Unit* u) {
-        if (next_whole < F) {
-            *u = W8Unit{next_whole, 0, chunks, -1};
-            next_whole += P;
+    __device__ __forceinline__ bool next(const W8TcArgs& a, int pair, int pairs, W8Unit* u) {
+        if (t < a.F) {
+            *u = W8Unit{mt, ot, 0, a.chunks, -1};
+            t += pairs;
+            mt += a.step_m;
+            ot += a.step_o;
+            if (mt >= a.tiles_m) {
+                mt -= a.tiles_m;
+                ++ot;
+            }
             return true;
         }
         if (c >= c1) return false;
-        const int t = static_cast<int>(c / chunks);
-        u->tile = F + t;
-        u->kb0 = static_cast<int>(c) - t * chunks;
-        u->kb1 = min(chunks, u->kb0 + static_cast<int>(c1 - c));
-        u->part = (u->kb0 == 0 && u->kb1 == chunks) ? -1 : 2 * p + (cut_units > 0 ? 1 : 0);
+        const int tile = static_cast<int>(c / a.chunks);
+        u->mt = (a.F + tile) % a.tiles_m;
+        u->ot = (a.F + tile) / a.tiles_m;
+        u->kb0 = static_cast<int>(c) - tile * a.chunks;
+        u->kb1 = min(a.chunks, u->kb0 + static_cast<int>(c1 - c));
+        u->part = (u->kb0 == 0 && u->kb1 == a.chunks) ? -1 : 2 * pair + (cut_units > 0 ? 1 : 0);
         ++cut_units;
         c += u->kb1 - u->kb0;
         return true;
@@ -254,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
     const uint32_t tmem_d = *tmem_slot;
     pdl_launch_dependents();
 
-    W8Walk walk(a, pair, pairs);
+    W8Walk walk(a, pair);
     W8Unit u;
     const uint32_t stage0 = smem_u32(base), full0 = smem_u32(full), empty0 = smem_u32(empty);
     if (warp == 0) {
@@ -272,17 +269,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         // before the tokens' codes are waited for: the first NS stages.
         int early = 0;
         if (a.early) {
-            W8Walk ahead(a, pair, pairs);
-            while (early < NS && ahead.next(&u)) {
-                const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
+            W8Walk ahead(a, pair);
+            while (early < NS && ahead.next(a, pair, pairs, &u)) {
+                const int o0 = u.ot * kW8Rows + static_cast<int>(rank) * 128;
                 for (int kb = u.kb0; kb < u.kb1 && early < NS; ++kb, ++early) load_weights(early, kb, o0);
             }
         }
         pdl_wait();
         int n = 0;
-        while (ok && walk.next(&u)) {
-            const int m0 = (u.tile % a.tiles_m) * TN + static_cast<int>(rank) * (TN / 2);
-            const int o0 = (u.tile / a.tiles_m) * kW8Rows + static_cast<int>(rank) * 128;
+        while (ok && walk.next(a, pair, pairs, &u)) {
+            const int m0 = u.mt * TN + static_cast<int>(rank) * (TN / 2);
+            const int o0 = u.ot * kW8Rows + static_cast<int>(rank) * 128;
             for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
                 if (round > 0 && !warp_wait_bounded(&empty[s], (round - 1) & 1u, abort_flag, kErrTimeoutEmpty)) {
                     ok = false;
@@ -315,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
             bool ok = true;
             int s = 0, i = 0;
             uint32_t phase = 0;
-            while (ok && walk.next(&u)) {
+            while (ok && walk.next(a, pair, pairs, &u)) {
                 const int buf = i & 1;
                 if (i >= 2) ok = warp_wait_bounded(&acc_empty[buf], ((i >> 1) - 1) & 1u, abort_flag, kErrTimeoutAccum);
                 if (!ok) break;
@@ -346,16 +343,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
         constexpr int kBlocks = TN >= 64 ? TN / 64 : 1;
         const int cbase = half * kBlocks * 32;  // TN = 32: the second half has nothing
         uint32_t* stage = reinterpret_cast<uint32_t*>(epi) + (warp - 2) * 16 * kW8PairStride;
-        uint16_t* stage4 = reinterpret_cast<uint16_t*>(epi + half * 4 * 16 * kW8PairStride * 4);
         float* scales = reinterpret_cast<float*>(epi + kW8EpiWarps * 16 * kW8PairStride * 4) + (warp - 2) * 128;
-        const bool whole16 = (out & 7) == 0;
         int i = 0;
         pdl_wait();
-        while (walk.next(&u)) {
+        while (walk.next(a, pair, pairs, &u)) {
             const int buf = i & 1;
-            const int m0 = (u.tile % a.tiles_m) * TN + cbase;
+            const int m0 = u.mt * TN + cbase;
             const int row = static_cast<int>(rank) * 128 + 32 * q + lane;      // in the tile
-            const int o0 = (u.tile / a.tiles_m) * kW8Rows;
+            const int o0 = u.ot * kW8Rows;
             const int o = o0 + row;
             const bool ov = o < out;
             // scales and bias come in while the products still run
@@ -368,10 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
                 scales[32 * b + lane] = 32 * b + lane < tokens ? a.p.a_scales[m0 + 32 * b + lane] : 0.0f;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, abort_flag,
                                                                       kErrTimeoutAccum));
-            bool go = !__any_sync(0xFFFFFFFFu, !ok || *abort_flag);
-            // four warps that will meet at barriers go on, or give up, together
-            if (!whole16) go = named_barrier_and(1 + half, 128, go);
-            if (!go) break;
+            if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) break;
             tc_fence_after();
             const uint32_t acc =
                 tmem_d + static_cast<uint32_t>(buf * TN + cbase) + (static_cast<uint32_t>(32 * q) << 16);
@@ -421,38 +413,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
                                            prmt(v1.x, v1.y, 0x7632u), prmt(v1.z, v1.w, 0x7632u));
                     }
                 } else {
-                    // rows of Y start anywhere: four warps put 128 outputs of the 32 tokens together and
-                    // store the whole 16 bytes among them as such (2 bytes a lane cost 10 cycles a store)
+                    // rows of Y that are not whole 16 bytes: 32 outputs of a token, 2 bytes a lane (put
+                    // together to 16-byte stores by four warps, the longer code took more than it gave)
+                    uint16_t* dst = a.p.Y + static_cast<size_t>(mb) * out + o;
+                    const int left = ov ? a.p.M - mb : 0;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        stage4[2 * e * kW8TokenStride + 32 * q + lane] = static_cast<uint16_t>(y[e]);
-                        stage4[(2 * e + 1) * kW8TokenStride + 32 * q + lane] = static_cast<uint16_t>(y[e] >> 16);
+                        if (2 * e < left) *dst = static_cast<uint16_t>(y[e]);
+                        dst += out;
+                        if (2 * e + 1 < left) *dst = static_cast<uint16_t>(y[e] >> 16);
+                        dst += out;
                     }
-                    named_barrier_sync(1 + half, 128);
-                    const int oc = o0 + static_cast<int>(rank) * 128;      // first output of the CTA's rows
-                    const int valid = min(128, out - oc), live = min(32, tokens - 32 * b);
-                    // 16 chunks, and 16 single outputs around them, of 8 tokens at a time
-                    const int sub = (32 * q + lane) >> 4, j = lane & 15;
-                    for (int tok = sub; tok < live; tok += 8) {
-                        const size_t row0 = static_cast<size_t>(mb + tok) * out + oc;
-                        const uint16_t* src = stage4 + tok * kW8TokenStride;
-                        const int head = static_cast<int>(-static_cast<int>(row0 & 7) & 7);   // outputs before the chunks
-                        const int e0 = head + 8 * j;
-                        if (e0 + 8 <= valid) {
-                            const uint32_t* w = reinterpret_cast<const uint32_t*>(src + (e0 & ~1));
-                            const uint32_t sh = (e0 & 1) * 16;
-                            uint32_t v[5];
-#pragma unroll
-                            for (int k = 0; k < 5; ++k) v[k] = w[k];
-                            *reinterpret_cast<uint4*>(a.p.Y + row0 + e0) =
-                                make_uint4(__funnelshift_r(v[0], v[1], sh), __funnelshift_r(v[1], v[2], sh),
-                                           __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
-                        }
-                        const int chunks = valid > head ? (valid - head) >> 3 : 0;
-                        const int single = j < 8 ? j : head + 8 * chunks + j - 8;
-                        if (j < 8 ? j < min(head, valid) : single < valid && single >= head) a.p.Y[row0 + single] = src[single];
-                    }
-                    named_barrier_sync(1 + half, 128);
                 }
             }
             // this warp's reads of the buffer are complete
