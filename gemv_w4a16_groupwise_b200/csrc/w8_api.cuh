@@ -9,7 +9,8 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 w4_status check_w8(int M, int N, int K, long long ldw, int transposed, const void* W, const void* bias,
                    const void* Y) {
     if (M <= 0 || N <= 0 || K <= 0 || ldw < K || !W || !Y) return W4_ERR_INVALID_ARG;
-    if ((transposed ? N : K) > w4::kW8MaxReduction) return W4_ERR_UNSUPPORTED;
+    if ((transposed ? N : K) > w4::kW8MaxReduction || std::max(M, std::max(N, K)) > (1 << 30))
+        return W4_ERR_UNSUPPORTED;
     if (!aligned16(W) || !aligned16(Y) || (bias && !aligned16(bias)) || ldw % 16 != 0) return W4_ERR_ALIGNMENT;
     return W4_OK;
 }
@@ -210,6 +211,7 @@ extern "C" {
 w4_status w8_quantize_rows(const void* X, int R, int C, const float* channel_scales, int8_t* codes, long long ld,
                            float* scales, void* stream) {
     if (R <= 0 || C <= 0 || ld < C || !X || !codes || !scales) return W4_ERR_INVALID_ARG;
+    if (std::max(R, C) > (1 << 30)) return W4_ERR_UNSUPPORTED;
     if (!aligned16(X) || !aligned16(codes) || !aligned16(scales) || !aligned16(channel_scales) || ld % 16 != 0)
         return W4_ERR_ALIGNMENT;
     return run_quantize_rows(static_cast<const uint16_t*>(X), R, C, channel_scales, codes, ld, scales,

@@ -228,7 +228,7 @@ w4_status w4_invert_permutation(const int32_t *perm, int n, int32_t *inv, void *
  * (rows = channels), on tokens, and, with channel_scales = the weights' scales,
  * on the gradients dY of the transposed product.
  * Validation: R, C > 0; ld >= C; X, codes, scales non-NULL (W4_ERR_INVALID_ARG);
- * pointers 16-byte aligned and ld a multiple of 16 (W4_ERR_ALIGNMENT).
+ * R, C at most 2^30 (W4_ERR_UNSUPPORTED); pointers 16-byte aligned and ld a multiple of 16 (W4_ERR_ALIGNMENT).
  */
 w4_status w8_quantize_rows(const void *X, int R, int C, const float *channel_scales, int8_t *codes,
                            long long ld, float *scales, void *stream);
@@ -251,7 +251,8 @@ size_t w8a8_linear_workspace_bytes(int M, int N, int K, int transposed);
  * taken, -128 included.
  * Validation: M, N, K > 0; lda, ldw >= their row lengths; pointers non-NULL
  * (bias may be NULL, w_scales as above); the length of the sum (K, transposed
- * N) at most 131071, beyond which int32 could overflow (W4_ERR_UNSUPPORTED);
+ * N) at most 131071, beyond which int32 could overflow, and M, N, K at most
+ * 2^30 (W4_ERR_UNSUPPORTED);
  * pointers 16-byte aligned, lda and ldw multiples of 16 (W4_ERR_ALIGNMENT);
  * workspace_bytes >= w8a8_workspace_bytes (W4_ERR_WORKSPACE).
  */
@@ -285,7 +286,7 @@ w4_status w8a8_linear(const void *A, int M, int N, int K, const int8_t *W, long 
  * takes.  residual may be x or y (in place).
  *   gate_kind: W4_GATE_NONE, W4_GATE_CHANNEL (bf16 [C]), W4_GATE_TOKEN (bf16 [M, C]).
  * All rows are bf16, dense.  Statistics are fp32.
- * Validation: M, C > 0; C <= 16384 (W4_ERR_UNSUPPORTED); gate_kind in range;
+ * Validation: M, C > 0; C <= 16384, M <= 2^30 (W4_ERR_UNSUPPORTED); gate_kind in range;
  * eps > 0 and finite; x, pre_weight, normed non-NULL; residual non-NULL exactly
  * when y is; with scales ld >= C; pointers (and ld) 16-byte aligned.
  */

@@ -216,6 +216,45 @@ def test_transposed_is_the_adjoint(cuda_device):
     assert abs((dx * X.double()).sum() - true) <= (X.double().abs() * bx).sum()
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 6])
+@pytest.mark.parametrize("K", [64, 1000, 4096])
+def test_poisoned_and_zero_tokens_of_a_small_batch(cuda_device, M, K):
+    """A token with a NaN or an infinity is NaN throughout and its neighbours are what they are
+    alone; a token of zeros gives the bias; weights with scale 0 or NaN reach their channel only."""
+    dev = cuda_device
+    N = 100
+    g = _gen(M + K, dev)
+    X = torch.randn(M, K, generator=g, device=dev).to(torch.bfloat16)
+    Wb = torch.randn(N, K, generator=g, device=dev).to(torch.bfloat16)
+    Wb[7] = 0
+    Wb[9, K - 1] = float("nan")
+    W, ws = w4.w8_quantize_rows(Wb)
+    b = torch.randn(N, generator=g, device=dev).to(torch.bfloat16)
+    clean = w4.w8a8_linear(X, W, ws, bias=b)
+    assert torch.isnan(clean[:, 9]).all() and torch.equal(clean[:, 7], b[7].expand(M))
+    fine = [n for n in range(N) if n != 9]
+    assert torch.isfinite(clean[:, fine]).all()
+    for bad in (float("nan"), float("inf"), float("-inf"), 0.0):
+        X2 = X.clone()
+        if bad == 0.0:
+            X2[M - 1] = 0
+        else:
+            X2[M - 1, K // 2] = bad
+        y = w4.w8a8_linear(X2, W, ws, bias=b)
+        assert torch.equal(y[:M - 1, fine], clean[:M - 1, fine])
+        if bad == 0.0:
+            assert torch.equal(y[M - 1, fine], b[fine])
+        else:
+            assert torch.isnan(y[M - 1]).all()
+
+
+@pytest.mark.parametrize("M,N,K,tr", [(40, 4096, 14336, False), (5, 3000, 130000, False), (20, 120000, 256, True),
+                                      (130, 512, 20000, False), (600, 1024, 9000, True)])
+def test_product_with_a_cut_reduction(cuda_device, M, N, K, tr):
+    """Long sums over few tiles, whose reduction is shared by many blocks."""
+    _check_product(M, N, K, tr, cuda_device, seed=M)
+
+
 # ------------------------------------------------------------- use
 def test_graph_replays_and_two_streams(cuda_device):
     dev = cuda_device
@@ -251,6 +290,37 @@ def test_graph_replays_and_two_streams(cuda_device):
     for o, x in zip(graphs[0][1], x2):
         assert torch.equal(o, w4.w8a8_linear(x, W, ws))
     assert w4.w4_device_error() == 0
+
+
+def test_first_calls_of_a_process_can_be_captured(cuda_device):
+    """A fresh process whose first calls are made under stream capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(w4.__file__)))
+    code = """
+import torch, gemv_w4a16_groupwise_b200 as w4
+x = torch.randn(20, 512, device="cuda").to(torch.bfloat16)
+w = torch.randn(640, 512, device="cuda").to(torch.bfloat16)
+pre = torch.ones(512, device="cuda", dtype=torch.bfloat16)
+def calls():
+    W, ws = w4.w8_quantize_rows(w)
+    f = w4.w4_block_norm(x, x, pre_weight=pre, quantize=True, keep_rstd=True)
+    y = w4.w8a8_gemm(f.normed, f.scales, W, ws)
+    d = w4.w8a8_linear(y, W, ws, transposed=True)
+    return [y, w4.w8a8_linear(x[:2], W, ws), *w4.w4_block_norm_backward(d, f.residual, f.rstd, x, pre_weight=pre)[:3]]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = calls()
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(out, calls()):
+    assert torch.equal(a, b)
+assert w4.w4_device_error() == 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_weights_written_right_before_the_product(cuda_device):

@@ -79,6 +79,7 @@ def test_quantize_rows_refusals():
     assert f(FAKE + 2, 4, 8, None, FAKE, 16, FAKE, None) == 3
     assert f(FAKE, 4, 8, FAKE + 4, FAKE, 16, FAKE, None) == 3
     assert f(FAKE, 4, 8, None, FAKE, 24, FAKE, None) == 3
+    assert f(FAKE, 4, (1 << 30) + 16, None, FAKE, 1 << 31, FAKE, None) == 2
 
 
 def _gemm_args(**k):
@@ -91,7 +92,7 @@ def _gemm_args(**k):
 @pytest.mark.parametrize("want,change", [
     (1, dict(M=0)), (1, dict(N=-1)), (1, dict(K=0)), (1, dict(ldw=48)), (1, dict(lda=48)), (1, dict(W=None)),
     (1, dict(A=None)), (1, dict(a_s=None)), (1, dict(Y=None)), (1, dict(w_s=None)), (1, dict(tr=1)),
-    (2, dict(K=131072, lda=131072, ldw=131072)), (2, dict(tr=1, N=131072, w_s=None, lda=131072)),
+    (2, dict(K=131072, lda=131072, ldw=131072)), (2, dict(M=(1 << 30) + 1)), (2, dict(N=(1 << 30) + 1)), (2, dict(tr=1, N=131072, w_s=None, lda=131072)),
     (3, dict(lda=72)), (3, dict(ldw=72)), (3, dict(A=FAKE + 8)), (3, dict(bias=FAKE + 2)), (3, dict(Y=FAKE + 4))])
 def test_gemm_refusals(want, change):
     assert w4.library().w8a8_gemm(*_gemm_args(**change)) == want
@@ -115,7 +116,7 @@ def _norm_args(**k):
 
 
 @pytest.mark.parametrize("want,change", [
-    (1, dict(M=0)), (1, dict(C=0)), (2, dict(C=16385)), (1, dict(kind=3, gate=FAKE)), (1, dict(kind=1)),
+    (1, dict(M=0)), (1, dict(C=0)), (2, dict(C=16385)), (2, dict(M=(1 << 30) + 1)), (1, dict(kind=3, gate=FAKE)), (1, dict(kind=1)),
     (1, dict(gate=FAKE)), (1, dict(eps=0.0)), (1, dict(eps=-1.0)), (1, dict(eps=float("nan"))),
     (1, dict(eps=float("inf"))), (1, dict(x=None)), (1, dict(pre=None)), (1, dict(n=None)), (1, dict(r=None)),
     (1, dict(y=None)), (1, dict(y=None, r=None, post=FAKE)), (1, dict(y=None, r=None, gate=FAKE, kind=1)),
