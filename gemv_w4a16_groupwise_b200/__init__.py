@@ -4,7 +4,9 @@ Every step of the computation runs in the library's sm_100a kernels; this
 module only checks tensor metadata, passes device pointers and the current
 CUDA stream, and turns status codes into exceptions.  PyTorch provides
 device memory and streams.  There is no CPU fallback: without a CUDA device
-or without the built library every call raises.
+or without the built library every call raises.  The calls of the 8-bit layer and
+of the block norms go through a native module (``binding/w8_native.cpp``) that
+does the same checks and allocations in C++.
 
 Entry points (same names as the C ABI in ``include/w4a16.h``):
 
@@ -413,16 +415,28 @@ def w4_scatter_columns(A, idx, dst_cols: int, out=None):
 
 
 # The 8-bit layer's and the block norms' calls take a few microseconds of
-# device time on a few tokens, so their checks are first made as one chain of
-# cheap attribute tests; whatever fails there goes through the checks that say
-# what is wrong.
+# device time on a few tokens, less than Python needs for their checks and
+# tensors.  An ordinary call is made by the native module (binding/
+# w8_native.cpp) in one C function; where that finds an argument it does not
+# take (None), the call goes through the checks here, which say what is wrong.
 class _Torch:
-    """torch and what the calls below use of it, looked up once."""
+    """torch, what the calls below use of it, and the native calls, looked up once."""
     torch = None
+    native = None
 
     @classmethod
     def load(cls):
         torch = _torch()
+        import importlib.machinery
+        import importlib.util
+        loader = importlib.machinery.ExtensionFileLoader("w8_native", _build.build_binding())
+        native = importlib.util.module_from_spec(importlib.util.spec_from_loader("w8_native", loader))
+        loader.exec_module(native)
+        lib = library()
+        native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "w8_quantize_rows", "w8a8_workspace_bytes", "w8a8_linear_workspace_bytes", "w8a8_gemm", "w8a8_linear",
+            "w4_block_norm", "w4_block_norm_workspace_bytes", "w4_block_norm_backward")))
+        cls.native = native
         cls.bf16, cls.f32, cls.i8, cls.u8 = torch.bfloat16, torch.float32, torch.int8, torch.uint8
         cls.empty_like = torch.empty_like
         cls.get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -430,6 +444,12 @@ class _Torch:
         cls.stream = raw or (lambda idx: torch.cuda.current_stream(idx).cuda_stream)
         cls.lib = library()
         cls.torch = torch
+
+
+def _native():
+    if _Torch.torch is None:
+        _Torch.load()
+    return _Torch.native
 
 
 def _call(name, dev, *args):
@@ -511,6 +531,12 @@ def w8_quantize_rows(X, channel_scales=None, out=None):
     The codes' rows start every multiple of 16 bytes (a view of a wider tensor
     when C is not one).  A row of zeros has scale 0, a row with an infinity or a
     NaN scale NaN and codes 0.  ``out``: (codes, scales) to write into."""
+    if out is None:
+        r = _native().quantize_rows(X, channel_scales)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            raise W4Error(r, "w8_quantize_rows")
     dev = _check_first(X, "X")
     R, C = X.shape
     if channel_scales is not None:
@@ -565,8 +591,11 @@ def w8a8_gemm(A, a_scales, codes, scales=None, *, bias=None, transposed: bool = 
     dX[m, k] = a_scales[m] sum_n A[m, n] codes[n, k] + bias[k], where A holds the rows of
     dY quantized with ``channel_scales=scales`` and ``scales`` is left out here.
     bf16 output; ``out`` may not overlap the inputs."""
-    if _Torch.torch is None:
-        _Torch.load()
+    r = _native().gemm(A, a_scales, codes, scales, bias, transposed, out)
+    if r is not None:
+        if r.__class__ is int:
+            raise W4Error(r, "w8a8_gemm")
+        return r
     tr = 1 if transposed else 0
     if tr and scales is not None:
         raise ValueError("transposed: fold the weights' scales into A "
@@ -589,6 +618,11 @@ def w8a8_linear(A, codes, scales, *, bias=None, transposed: bool = False, out=No
     """8-bit linear layer on bf16 rows: :func:`w8_quantize_rows` on A and
     :func:`w8a8_gemm` in one call.  Y = A . dequant(codes)^T (A [M, K]), or,
     transposed, dX = A . dequant(codes) (A [M, N]).  ``out`` may not overlap the inputs."""
+    r = _native().linear(A, codes, scales, bias, transposed, out)
+    if r is not None:
+        if r.__class__ is int:
+            raise W4Error(r, "w8a8_linear")
+        return r
     dev = _check_first(A, "A")
     if scales is None:
         raise ValueError("scales of the weights are needed")
@@ -651,6 +685,12 @@ def w4_block_norm(x, y=None, *, pre_weight, post_weight=None, gate=None, residua
     w + weight_offset.  gate: bf16 [C] or [M, C].  ``quantize`` gives the normed rows as
     int8 codes and scales for :func:`w8a8_gemm` instead of bf16.  ``keep_rstd`` keeps what
     :func:`w4_block_norm_backward` needs.  ``residual_out`` may be x or y (in place)."""
+    r = _native().norm(x, y, pre_weight, post_weight, gate, residual_scale, weight_offset, eps, quantize, keep_rstd,
+                       residual_out)
+    if r is not None:
+        if r.__class__ is int:
+            raise W4Error(r, "w4_block_norm")
+        return BlockNorm._make(r)
     dev = _check_first(x, "x")
     M, C = x.shape
     kind = _check_norm(M, C, dev, pre_weight, post_weight, gate, y)
@@ -681,6 +721,12 @@ def w4_block_norm_backward(d_normed, residual, rstd, y=None, *, d_residual=None,
 
     All bf16: d_x, d_y [M, C], d_pre_weight, d_post_weight [C], d_gate in the gate's shape.
     Quantized rows count as the values they stand for.  The same inputs give the same bits."""
+    r = _native().norm_backward(d_normed, residual, rstd, d_residual, y, pre_weight, post_weight, gate, residual_scale,
+                                weight_offset)
+    if r is not None:
+        if r.__class__ is int:
+            raise W4Error(r, "w4_block_norm_backward")
+        return BlockNormGrad._make(r)
     dev = _check_first(d_normed, "d_normed")
     M, C = d_normed.shape
     bf16, empty_like = _Torch.bf16, _Torch.empty_like

@@ -1,4 +1,5 @@
-"""Build the in-tree CUDA library ``libw4a16.so`` for sm_100a with nvcc."""
+"""Build the in-tree CUDA library ``libw4a16.so`` for sm_100a with nvcc, and the native part of
+the Python binding, ``w8_native.so``, with the host compiler."""
 from __future__ import annotations
 
 import glob
@@ -11,6 +12,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a16.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING = os.path.join(HERE, "binding", "w8_native.cpp")
+BINDING_LIB = os.path.join(HERE, "w8_native.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -48,5 +51,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The native calls of the binding: a CPython module against PyTorch's headers.  It reaches
+    the CUDA library through function addresses, so it does not link to it."""
+    header = os.path.join(INCLUDE, "w4a16.h")
+    if (not force and os.path.exists(BINDING_LIB)
+            and all(os.path.getmtime(f) <= os.path.getmtime(BINDING_LIB) for f in (BINDING, header))):
+        return BINDING_LIB
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(), cuda]
+    tmp = BINDING_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in includes], BINDING, "-o", tmp,
+           *[f"-L{d}" for d in cpp_extension.library_paths()], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
+
+
 if __name__ == "__main__":
+    print(build_binding(force="--force" in sys.argv, verbose=True))
     print(build(force="--force" in sys.argv, verbose=True))

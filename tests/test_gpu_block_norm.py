@@ -239,6 +239,19 @@ def test_blocks_in_a_row(cuda_device, M):
     assert w4.w4_device_error() == 0
 
 
+def test_arguments_the_native_call_leaves(cuda_device):
+    """Whole-number scales and offsets go through the Python checks to the same kernel."""
+    s = _case(9, 200, True, "token", cuda_device)
+    a, b = _call(s, 1.0, 0.0, keep_rstd=True), _call(s, 1, 0, keep_rstd=True)
+    for p, q in zip(a, b):
+        assert (p is None and q is None) or torch.equal(p, q)
+    for p, q in zip(_backward(s, a, 1.0, 0.0), _backward(s, b, 1, 0)):
+        assert torch.equal(p, q)
+    w = torch.nn.Parameter(s["pre"])
+    assert torch.equal(w4.w4_block_norm(s["x"], s["y"], pre_weight=w).normed,
+                       w4.w4_block_norm(s["x"], s["y"], pre_weight=s["pre"]).normed)
+
+
 def test_binding_refusals(cuda_device):
     dev = cuda_device
     s = _case(4, 64, True, "channel", dev)

@@ -347,6 +347,29 @@ def test_weights_written_right_before_the_product(cuda_device):
             assert torch.equal(p, q)
 
 
+def test_parameters_out_and_odd_arguments(cuda_device):
+    """What the native calls take, leave to the Python checks, and give back."""
+    dev = cuda_device
+    X = torch.nn.Parameter(torch.randn(5, 96, device=dev).to(torch.bfloat16))
+    W, ws = w4.w8_quantize_rows(torch.randn(40, 96, device=dev).to(torch.bfloat16))
+    y = w4.w8a8_linear(X, W, ws)
+    assert type(y) is torch.Tensor and not y.requires_grad and y.is_contiguous()
+    out = torch.empty_like(y)
+    assert w4.w8a8_linear(X, W, ws, out=out) is out and torch.equal(out, y)
+    a, a_s = w4.w8_quantize_rows(X)
+    assert w4.w8a8_gemm(a, a_s, W, ws, out=out) is out and torch.equal(out, y)
+    assert torch.equal(w4.w8a8_linear(X, W, ws, transposed=0), y)
+    one, one_s = w4.w8_quantize_rows(torch.randn(1, 96, device=dev).to(torch.bfloat16))   # a single weight row
+    got = w4.w8a8_linear(X, one, one_s)
+    wide = torch.cat([one, one])
+    assert torch.equal(got, w4.w8a8_linear(X, wide, one_s.repeat(2))[:, :1])
+    with torch.inference_mode():
+        assert torch.equal(w4.w8a8_linear(X, W, ws), y)
+    strided = torch.zeros(5, 200, dtype=torch.bfloat16, device=dev)[:, :96]
+    with pytest.raises(ValueError):
+        w4.w8a8_linear(strided, W, ws)
+
+
 def test_binding_refusals(cuda_device):
     dev = cuda_device
     q, s = torch.zeros(4, 32, dtype=torch.int8, device=dev), torch.ones(4, device=dev)

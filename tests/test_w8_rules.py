@@ -152,6 +152,20 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         w4.w8_quantize_rows([1.0])
 
 
+def test_native_calls_leave_what_they_do_not_take():
+    """The native module answers None, and raises nothing, for host tensors and odd arguments."""
+    native = w4._native()
+    x, q, s = torch.zeros(2, 16, dtype=torch.bfloat16), torch.zeros(4, 16, dtype=torch.int8), torch.ones(4)
+    assert native.quantize_rows(x, None) is None
+    assert native.quantize_rows(3, None) is None and native.quantize_rows(x) is None
+    assert native.gemm(q, s, q, s, None, False, None) is None and native.gemm(None, 1, 2, 3, 4, 5, 6) is None
+    assert native.linear(x, q, s, None, False, None) is None and native.linear(x) is None
+    assert native.norm(x, x, x[0], None, None, 1.0, 0.0, 1e-5, False, False, None) is None
+    assert native.norm_backward(x, x, s, None, None, x[0], None, None, 1.0, 0.0) is None
+    with pytest.raises(TypeError):
+        native.bind(1)
+
+
 def test_header_and_binding_agree_on_the_new_symbols():
     lib = ctypes.CDLL(w4.library_path())
     for name in ("w8_quantize_rows", "w8a8_gemm", "w8a8_linear", "w8a8_workspace_bytes",
