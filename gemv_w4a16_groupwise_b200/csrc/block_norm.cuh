@@ -15,9 +15,11 @@
 //     d_y    = rstd_y (dt - yh mean(dt yh))                (dt without a post norm)
 //     d_pre  = sum_m dn xh
 //
-// Both kernels are bound by device memory: a row is read once and held in
-// registers as bf16 (half the registers of fp32) between the reductions.
-// Sums and statistics are fp32 in a fixed order.
+// A row is read from device memory once; what a reduction separates stays in
+// registers as bf16 or is read again from shared memory.  Sums and statistics
+// are fp32 in a fixed order.  Measured on 4096 x 4096 with a post norm and a
+// gate per token: forward 28.2 us (5.9 TB/s, bound by memory), backward 56 us
+// (4.8 TB/s, bound by issue slots and the latency of a row's reductions).
 #pragma once
 
 #include "rows.cuh"

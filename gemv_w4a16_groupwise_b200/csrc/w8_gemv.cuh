@@ -9,7 +9,9 @@
 // mma.sync.m16n8k32 wants them: lane (g, t) holds bytes 16 t .. 16 t + 15 of a
 // piece of rows g and g + 8, and of token g; that the four words stand for
 // other k than the instruction's own order is the same on both sides.  The
-// integer sums of the warps are added in shared memory.
+// integer sums of the warps are added in shared memory.  1 x 28672 x 4096 in
+// 20.6 us (5.7 TB/s), 1 x 6144 x 4096 in 7.5 us; four blocks with half the loads
+// each take 28 and 9.8.
 //
 // MT > 0: bf16 tokens, quantized by every block for itself while its first
 // weights are on their way (up to 16384 values a block, from L2): one launch

@@ -131,7 +131,9 @@ __device__ __forceinline__ void unpack8(float2 (&v)[4], uint4 x) {
 
 // Rows of at most 16384: a block holds a row in registers between the maximum
 // and the codes, so the row is read once, and has the next row's loads under
-// way meanwhile.  Bound by device memory (3 bytes an element).  Every thread
+// way meanwhile.  Bound by device memory (3 bytes an element): 4096 x 16384 in
+// 31 us (6.4 TB/s); 4096 x 4096 in 10.3 us, where launch and latency show.  Every
+// thread
 // keeps the channel factors of its columns (twice a row's bytes) in shared
 // memory, 16 bytes of a thread beside its neighbours': from L1, 32 bytes apart,
 // they took most of the time of a row.
