@@ -19,12 +19,14 @@
 //
 // Warps: 0 TMA producer, 1 MMA issuer (in the pair's first CTA), 2..9
 // epilogue.  Accumulators are double buffered, so a tile's epilogue runs
-// beside the next tile's products.  Measured: 2048 x 28672 x 4096 in 151 us
-// (3.2 PFLOP/s, tensor pipe busy 90 % of the launch), bound by the products;
-// 33 x 28672 x 4096 in 22.3 us (5.3 TB/s), bound by the weights' bytes; a call
-// with one stage per tile in 4.6 to 6.5 us, bound by its own latency.  Full barriers live in the first CTA and
+// beside the next tile's products.  Full barriers live in the first CTA and
 // count both CTAs' bytes; the stage's release and the accumulator's
 // completion are committed to both.
+//
+// Measured: 2048 x 28672 x 4096 in 151 us (3.2 PFLOP/s, tensor pipe busy 90 %
+// of the launch), bound by the products; 33 x 28672 x 4096 in 22.3 us
+// (5.3 TB/s), bound by the weights' bytes; a call with one stage per tile in
+// 4.6 to 6.5 us, bound by its own latency.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -454,12 +456,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
     }
 }
 
-// The cut tiles: Y = bf16(sum of the partials * scales + bias).  Bound by its
-// reads from L2; with the share's arithmetic in 64 bits and per thread it took
-// 10 us more for 44 tiles of 256 x 256.  One thread
-// per token and four outputs, blocks (x, y): 256 threads of tile F + y; a tile
-// that one pair computed whole is already stored.  The pair whose share
+// The cut tiles: Y = bf16(sum of the partials * scales + bias).  One thread per
+// token and four outputs, blocks (x, y): 256 threads of tile F + y; a tile that
+// one pair computed whole is already stored.  The pair whose share
 // [total p / P, total (p + 1) / P) holds stage c is ((c + 1) P - 1) / total.
+// Bound by its reads from L2; with the share's arithmetic in 64 bits and per
+// thread it took 10 us more for 44 tiles of 256 x 256.
 template <bool TR>
 __global__ void __launch_bounds__(256) w8_finalize_kernel(const W8TcArgs a, int TN) {
     pdl_launch_dependents();

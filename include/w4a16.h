@@ -211,10 +211,8 @@ w4_status w4_invert_permutation(const int32_t *perm, int n, int32_t *inv, void *
 
 /*
  * 8-bit integers.  The same layer with int8 weights and int8 tokens: one fp32
- * scale per weight row (channel) and one per token row, as in the scaled
- * product that vLLM "Adding bias epilogue support for cutlass_scaled_mm" adds
- * its bias epilogue to.  Codes are int8 rows, `ld` bytes apart, ld a multiple
- * of 16 and at least the row length rounded up to 16 (so that rows start on 16
+ * scale per weight row (channel) and one per token row.  Codes are int8 rows,
+ * `ld` bytes apart, ld a multiple of 16 and at least the row length rounded up to 16 (so that rows start on 16
  * bytes and may be read in 16-byte pieces; what lies behind the row length is
  * never used).  Scales are fp32.
  *
