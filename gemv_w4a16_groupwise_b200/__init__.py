@@ -435,7 +435,7 @@ class _Torch:
         lib = library()
         native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "w8_quantize_rows", "w8a8_workspace_bytes", "w8a8_linear_workspace_bytes", "w8a8_gemm", "w8a8_linear",
-            "w4_block_norm", "w4_block_norm_workspace_bytes", "w4_block_norm_backward")))
+            "w4_block_norm", "w4_block_norm_workspace_bytes", "w4_block_norm_backward")), BlockNorm, BlockNormGrad)
         cls.native = native
         cls.bf16, cls.f32, cls.i8, cls.u8 = torch.bfloat16, torch.float32, torch.int8, torch.uint8
         cls.empty_like = torch.empty_like
@@ -690,7 +690,7 @@ def w4_block_norm(x, y=None, *, pre_weight, post_weight=None, gate=None, residua
     if r is not None:
         if r.__class__ is int:
             raise W4Error(r, "w4_block_norm")
-        return BlockNorm._make(r)
+        return r
     dev = _check_first(x, "x")
     M, C = x.shape
     kind = _check_norm(M, C, dev, pre_weight, post_weight, gate, y)
@@ -726,7 +726,7 @@ def w4_block_norm_backward(d_normed, residual, rstd, y=None, *, d_residual=None,
     if r is not None:
         if r.__class__ is int:
             raise W4Error(r, "w4_block_norm_backward")
-        return BlockNormGrad._make(r)
+        return r
     dev = _check_first(d_normed, "d_normed")
     M, C = d_normed.shape
     bf16, empty_like = _Torch.bf16, _Torch.empty_like

@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -31,6 +31,9 @@ struct Api {
     decltype(&w4_block_norm_workspace_bytes) norm_workspace;
     decltype(&w4_block_norm_backward) norm_backward;
 } api;
+
+PyTypeObject* block_norm_type = nullptr;         // named tuples of the Python module
+PyTypeObject* block_norm_grad_type = nullptr;
 
 constexpr int64_t kMost = 1ll << 30;
 
@@ -75,7 +78,8 @@ int64_t codes_stride(const at::Tensor* t, c10::DeviceIndex dev) {
 }
 
 at::Tensor empty_like_type(const at::Tensor& like, at::IntArrayRef sizes, at::ScalarType type) {
-    return at::empty(sizes, like.options().dtype(type).requires_grad(false));
+    // what at::empty comes to on a CUDA device, without the dispatcher
+    return at::detail::empty_cuda(sizes, type, like.device(), c10::nullopt);
 }
 at::Tensor empty_codes(const at::Tensor& like, int64_t R, int64_t C) {
     at::Tensor q = empty_like_type(like, {R, round16(C)}, at::kChar);
@@ -92,8 +96,10 @@ PyObject* wrap(const at::Tensor& t) {
     if (!t.defined()) Py_RETURN_NONE;
     return THPVariable_Wrap(t);
 }
-PyObject* tuple(std::initializer_list<at::Tensor> ts) {
-    PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
+// The tensors as a tuple, or as the named tuple `type`.
+PyObject* tuple(std::initializer_list<at::Tensor> ts, PyTypeObject* type = &PyTuple_Type) {
+    const Py_ssize_t n = static_cast<Py_ssize_t>(ts.size());
+    PyObject* r = type == &PyTuple_Type ? PyTuple_New(n) : type->tp_alloc(type, n);
     if (!r) return nullptr;
     Py_ssize_t i = 0;
     for (const at::Tensor& t : ts) {
@@ -259,7 +265,7 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
                   normed.data_ptr(), round16(C), sc, rs, st_);
     Py_END_ALLOW_THREADS
     if (st != W4_OK) return PyLong_FromLong(st);
-    PyObject* t = tuple({residual, normed, scales, rstd});
+    PyObject* t = tuple({residual, normed, scales, rstd}, block_norm_type);
     // what the caller gave comes back as the caller's own object
     PyObject* own = !in.y ? args[0] : given ? args[10] : nullptr;
     if (t && own) {
@@ -302,23 +308,33 @@ PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
                            pdy, dpre.data_ptr(), pdpost, pdgate, ws.data_ptr(), bytes, st_);
     Py_END_ALLOW_THREADS
     if (st != W4_OK) return PyLong_FromLong(st);
-    return tuple({dx, dy, dpre, dpost, dgate});
+    return tuple({dx, dy, dpre, dpost, dgate}, block_norm_grad_type);
     END_HANDLE_TH_ERRORS
 }
 
-// The library's functions by address, in the order of Api.
+// The library's functions by address, in the order of Api, then the named
+// tuples of the norm's results and of its gradients.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    constexpr Py_ssize_t kFunctions = sizeof(Api) / sizeof(void*);
     void** f = reinterpret_cast<void**>(&api);
-    if (n != static_cast<Py_ssize_t>(sizeof(Api) / sizeof(void*))) {
-        PyErr_SetString(PyExc_TypeError, "bind: wrong number of functions");
+    if (n != kFunctions + 2) {
+        PyErr_SetString(PyExc_TypeError, "bind: wrong number of arguments");
         return nullptr;
     }
-    for (Py_ssize_t i = 0; i < n; ++i) {
+    for (Py_ssize_t i = 0; i < kFunctions; ++i) {
         f[i] = PyLong_AsVoidPtr(args[i]);
         if (!f[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: null function");
             return nullptr;
         }
+    }
+    for (Py_ssize_t i = kFunctions; i < n; ++i) {
+        if (!PyType_Check(args[i]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(args[i]), &PyTuple_Type)) {
+            PyErr_SetString(PyExc_TypeError, "bind: a tuple type is needed");
+            return nullptr;
+        }
+        Py_INCREF(args[i]);
+        (i == kFunctions ? block_norm_type : block_norm_grad_type) = reinterpret_cast<PyTypeObject*>(args[i]);
     }
     Py_RETURN_NONE;
 }
