@@ -4,7 +4,7 @@
 //
 // On a few tokens these calls take 2 to 10 us of device time, and the same
 // steps through Python attribute tests, tensor constructors and ctypes took
-// 8 to 11 us of the host's.  A function here returns the call's result; the
+// 8 to 11 us of the host's (here 3 to 4).  A function here returns the call's result; the
 // library's status (an int) where the library refuses the call; or None where
 // an argument is not what an ordinary call has, and then the Python binding
 // makes the call with its own checks, which say what is wrong.

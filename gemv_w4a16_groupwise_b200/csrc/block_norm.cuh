@@ -357,21 +357,26 @@ __global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_b
 }
 
 // out_k[c] = bf16(sum over the rows of slab k of the blocks' partial sums), in
-// a fixed order: a block takes 32 columns, its warps 4 rows each at a time
-// (8 lanes x 4 columns a row); the threads' sums are added in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int rows, int C,
-                                                          uint16_t* o0, uint16_t* o1, uint16_t* o2) {
-    __shared__ float s[32][33];
+// a fixed order: a block takes 32 columns, its WARPS warps 4 rows each at a time
+// (8 lanes x 4 columns a row); a warp adds its 4 rows by shuffles, then the
+// warps' sums are added in order.  Bound by latency: 16 warps halve the loads
+// that a thread makes one after the other (8192 x 1024 backward: 39 -> 34 us);
+// for a few dozen rows 8 are enough, and quicker to start (64 x 1024: 5.5
+// against 7.4 us).
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) column_sums_kernel(const float* __restrict__ part, int rows, int C,
+                                                                uint16_t* o0, uint16_t* o1, uint16_t* o2) {
+    __shared__ float4 s[WARPS][8];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const size_t stride = partial_stride(C);
     const float* p = part + static_cast<size_t>(blockIdx.y) * rows * stride;
-    const int quad = blockIdx.x * 32 + (lane & 7) * 4, r0 = warp * 4 + (lane >> 3);
+    const int quad = blockIdx.x * 32 + (lane & 7) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (quad < C) {                   // columns behind C are read and dropped
 #pragma unroll 8
-        for (int r = r0; r < rows; r += 32) {
+        for (int r = warp * 4 + (lane >> 3); r < rows; r += 4 * WARPS) {
             const float4 u = *reinterpret_cast<const float4*>(p + r * stride + quad);
             v.x += u.x;
             v.y += u.y;
@@ -379,14 +384,21 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
             v.w += u.w;
         }
     }
-    float* d = &s[r0][(lane & 7) * 4];
-    d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1) {
+        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+        v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, o);
+        v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, o);
+    }
+    if (lane < 8) s[warp][lane] = v;
     __syncthreads();
     const int c = blockIdx.x * 32 + lane;
     if (warp == 0 && c < C) {
+        const float* sums = reinterpret_cast<const float*>(s);
         float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 32; ++w) t += s[w][lane];
+        for (int w = 0; w < WARPS; ++w) t += sums[w * 32 + lane];
         uint16_t* o = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
         o[c] = to_bf16_bits(t);
     }

@@ -143,8 +143,12 @@ w4_status w4_block_norm_backward(const void* d_normed, const void* d_residual, c
     int k = 1;
     if (post_weight) o[k++] = static_cast<uint16_t*>(d_post_weight);
     if (chan) o[k++] = static_cast<uint16_t*>(d_gate);
-    launch_pdl(w4::column_sums_kernel, dim3((C + 31) / 32, sums), dim3(256), 0, st,
-               static_cast<const float*>(a.part), blocks, C, o[0], o[1], o[2]);
+    const dim3 grid((C + 31) / 32, sums);
+    const float* part = a.part;
+    if (blocks > 128)
+        launch_pdl(w4::column_sums_kernel<16>, grid, dim3(512), 0, st, part, blocks, C, o[0], o[1], o[2]);
+    else
+        launch_pdl(w4::column_sums_kernel<8>, grid, dim3(256), 0, st, part, blocks, C, o[0], o[1], o[2]);
     return launch_status();
 }
 

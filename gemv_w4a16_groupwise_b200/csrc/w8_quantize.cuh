@@ -132,13 +132,14 @@ __device__ __forceinline__ void unpack8(float2 (&v)[4], uint4 x) {
 // Rows of at most 16384: a block holds a row in registers between the maximum
 // and the codes, so the row is read once, and has the next row's loads under
 // way meanwhile.  Bound by device memory (3 bytes an element): 4096 x 16384 in
-// 31 us (6.4 TB/s); 4096 x 4096 in 10.3 us, where launch and latency show.  Every
-// thread
+// 31 us (6.4 TB/s), 28672 x 4096 in 53; 4096 x 4096 in 9.8 us, where launch and
+// latency show.  Every thread
 // keeps the channel factors of its columns (twice a row's bytes) in shared
 // memory, 16 bytes of a thread beside its neighbours': from L1, 32 bytes apart,
-// they took most of the time of a row.
-template <int T, int G, int VEC, bool CHANNEL>
-__global__ void __launch_bounds__(T, CHANNEL && G > 2 ? 1 : 1024 / T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
+// they took most of the time of a row.  THREADS: an SM's, 1024, or 1536 for some
+// shapes with many rows.
+template <int T, int G, int VEC, bool CHANNEL, int THREADS = 1024>
+__global__ void __launch_bounds__(T, CHANNEL && G > 2 ? 1 : THREADS / T) quantize_rows_kernel(const uint16_t* __restrict__ X, int R, int C,
                                                                     const float* __restrict__ channel,
                                                                     int8_t* __restrict__ codes, long long ld,
                                                                     float* __restrict__ scales) {

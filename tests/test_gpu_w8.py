@@ -66,7 +66,8 @@ def test_codes_are_the_exact_quotients_for_every_significand(cuda_device):
 
 
 @pytest.mark.parametrize("R,C", [(1, 1), (3, 7), (2, 16), (5, 100), (4, 1001), (7, 2048), (3, 4096), (2, 8200),
-                                 (3, 14336), (2, 28672), (2, 33000), (1, 128256), (700, 64)])
+                                 (3, 14336), (2, 28672), (2, 33000), (1, 128256), (700, 64), (2000, 4096), (7200, 999),
+                                 (1800, 6001), (1000, 8192)])
 @pytest.mark.parametrize("folded", [False, True])
 def test_quantize_rows(cuda_device, R, C, folded):
     dev = cuda_device
