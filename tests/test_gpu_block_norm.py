@@ -150,6 +150,26 @@ def test_zero_and_poisoned_rows(cuda_device, C):
     assert torch.equal(again.normed, f.normed[keep]) and torch.equal(again.residual, f.residual[keep])
 
 
+@pytest.mark.parametrize("C", [8192, 8191])
+def test_offsets_past_32_bits(cuda_device, C):
+    """More than 2^31 values in a tensor: rows at the end are what they are alone."""
+    dev = cuda_device
+    M = 2 ** 31 // C + 300
+    M += (M % 2) ^ 1                   # odd, so that odd rows begin at either half of a word
+    s = _case(8, C, True, "channel", dev)
+    big = {**s, **{k: s[k].repeat((M + 7) // 8, 1)[:M].contiguous() for k in ("x", "y", "dn", "dres")}}
+    f, q = _call(big, 0.5, 0.0, keep_rstd=True), _call(big, 0.5, 0.0, quantize=True)
+    g = _backward(big, f, 0.5, 0.0)
+    one = {**s, **{k: big[k][:8].contiguous() for k in ("x", "y", "dn", "dres")}}
+    f1, q1 = _call(one, 0.5, 0.0, keep_rstd=True), _call(one, 0.5, 0.0, quantize=True)
+    g1 = _backward(one, f1, 0.5, 0.0)
+    for lo in (0, 8 * (M // 16), (M // 8 - 1) * 8):
+        at = slice(lo, lo + 8)
+        assert torch.equal(f.residual[at], f1.residual) and torch.equal(f.normed[at], f1.normed)
+        assert torch.equal(q.normed[at], q1.normed) and torch.equal(q.scales[at], q1.scales)
+        assert torch.equal(g.d_x[at], g1.d_x) and torch.equal(g.d_y[at], g1.d_y)
+
+
 def test_zero_scale_leaves_the_residual(cuda_device):
     s = _case(4, 320, True, "token", cuda_device)
     assert torch.equal(_call(s, 0.0, 0.0).residual, s["x"])

@@ -256,6 +256,29 @@ def test_product_with_a_cut_reduction(cuda_device, M, N, K, tr):
     _check_product(M, N, K, tr, cuda_device, seed=M)
 
 
+def test_offsets_past_32_bits(cuda_device):
+    """More than 2^31 values in the tokens, their codes and the output: rows at the end are what
+    they are alone."""
+    dev = cuda_device
+    M, N, K = 70000, 32000, 32000            # 2.24e9 elements each
+    g = _gen(3, dev)
+    X = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    for lo in range(0, M, 10000):
+        X[lo:lo + 10000] = torch.randn(min(10000, M - lo), K, generator=g, device=dev)
+    W, ws = w4.w8_quantize_rows(torch.randn(N, K, generator=g, device=dev).to(torch.bfloat16))
+    codes, scales = w4.w8_quantize_rows(X)
+    y = w4.w8a8_gemm(codes, scales, W, ws)
+    for lo in (0, 33000, 67100, 69990):       # 67109 rows of 32000 are 2^31 values
+        rows = X[lo:lo + 10].clone()
+        c, s = w4.w8_quantize_rows(rows)
+        assert torch.equal(codes[lo:lo + 10], c) and torch.equal(scales[lo:lo + 10], s)
+        assert torch.equal(y[lo:lo + 10], w4.w8a8_gemm(c, s, W, ws))
+    del y, codes
+    d = w4.w8a8_linear(X, W, ws, transposed=True)
+    for lo in (0, 69990):
+        assert torch.equal(d[lo:lo + 10], w4.w8a8_linear(X[lo:lo + 10].clone(), W, ws, transposed=True))
+
+
 # ------------------------------------------------------------- use
 def test_graph_replays_and_two_streams(cuda_device):
     dev = cuda_device
