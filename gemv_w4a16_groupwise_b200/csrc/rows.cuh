@@ -33,7 +33,8 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // words of the block's threads side by side: in a row that starts at an odd
 // value (`shift` = 1) the pairs begin at column -1, whose half belongs to the
 // row before.  A block's rows lie an even number of rows apart, so `shift` is
-// the same for all of them and a thread keeps its columns.
+// the same for all of them and a thread keeps its columns.  (A sum over an odd
+// row of odd width is thus added up in another order than over an even one.)
 template <int T, int G, int VEC>
 struct RowSpan {
     int shift;       // 1: the block's rows start in the middle of a word
