@@ -109,10 +109,11 @@ W8Plan plan_w8(int M, int N, int K, bool transposed, int sms) {
     W8Plan best;
     best.us = 1e30;
     for (int size = 0; size < 4; ++size) {
-        for (int cut = 0; cut < 2; ++cut) {
-            const W8Plan p = plan_w8_as(M, N, K, transposed, pairs, size, cut != 0);
-            if (p.us < best.us) best = p;
-        }
+        W8Plan p = plan_w8_as(M, N, K, transposed, pairs, size, false);
+        const W8Plan cut = plan_w8_as(M, N, K, transposed, pairs, size, true);
+        if (cut.us < p.us) p = cut;
+        // near ties go to the wider tile (777 x 4099 x 1001: 9.7 against 10.3 us)
+        if (p.us < 1.01 * best.us) best = p;
         if (M <= (32 << size)) break;    // a wider tile would only be emptier
     }
     return best;
