@@ -5,19 +5,29 @@
 // NaN.
 //
 // The quotient is not divided out per element: the code is rint(v inv), one
-// fma, with inv at least 127 / max |v| and above it by less than 2^-21 of it.
+// fma, with inv the least fp32 number that is not below 127 / max |v|, so above
+// it by less than 2^-23 of it.
+//
 // For bf16 v this is the exact quotient rounded half to even.  Write
 // v = i 2^-d and max |v| = b in units of the maximum's last place, b in
 // [128, 255], |i| <= 255: the quotient is 127 i 2^-d / b, and its distance from
 // a rounding border h + 1/2 is a multiple of 1 / (2^(d+1) b), at least 2^-(d+9)
-// when not zero, against less than 2^(8-d) 2^-21 from inv.  Ties: 254 i =
+// when not zero, against less than 2^(8-d) 2^-23 from inv.  Ties: 254 i =
 // (2h+1) b 2^d needs 127 to divide b or 2h + 1.  2h + 1 = 127 is |q| = 63.5,
 // which goes to 64, the even code and the side that inv leans to; b = 254 makes
-// 127 / max |v| a power of two, and inv is set to it exactly.
+// 127 / max |v| a power of two, which inv then is.
 //
-// inv is a reciprocal of the hardware's (within 2^-23) and a product: an IEEE
-// division in every thread of a row's block, and the scale's, cost more issue
-// slots than the row's own values.
+// For fp32 v (products with channel factors, normed rows) quotients lie as close
+// to a border as one likes, and 2^-23 gives about as many codes beside the exact
+// quotient's (1e-6 of them) as a division in fp32.  The nearest fp32 number
+// would halve that but send v = max / 2, which rows times one common factor are
+// full of, to 63 as often as to 64.
+//
+// inv is a reciprocal of the hardware's (within 2^-23) times 127, corrected by
+// what its product with the maximum leaves of 127 (one Newton step, which
+// leaves the rounding alone), and moved up by one where that is still positive:
+// an IEEE division in every thread of a row's block, and the scale's, cost more
+// issue slots than the row's own values.
 #pragma once
 
 #include "rows.cuh"
@@ -44,11 +54,10 @@ __device__ __forceinline__ RowCodes row_codes(float top) {
     top *= s.pre;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(top));
-    // 127 (1 + 2^-22), one ulp up: above the two roundings' 2^-23 + 2^-24
-    s.inv = r * 127.0000381f;
-    const uint32_t bits = __float_as_uint(top);
-    // 1.984375 2^e = 127 2^(e-6): the quotient is 2^(6-e)
-    if ((bits & 0x007FFFFFu) == 0x007E0000u) s.inv = __uint_as_float((260u - (bits >> 23)) << 23);
+    float i = 127.0f * r;
+    i = fmaf(fmaf(-i, top, 127.0f), r, i);
+    // the sign of 127 - i top survives its rounding
+    s.inv = fmaf(-i, top, 127.0f) > 0.0f ? __uint_as_float(__float_as_uint(i) + 1u) : i;
     if (!(top > 0.0f)) s.inv = 0.0f;
     return s;
 }
