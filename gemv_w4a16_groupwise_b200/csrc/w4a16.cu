@@ -60,6 +60,12 @@ DeviceInfo device_info(int dev) {
     return d;
 }
 
+// The stage that w4_debug_withhold_stage set on a device, for kernels that take it as an argument.
+std::atomic<int>& withheld_stage(int dev) {
+    static std::atomic<int> stage[64];       // 0: none, else the stage + 1
+    return stage[dev & 63];
+}
+
 int current_device() {
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1222,6 +1228,7 @@ w4_status w4_debug_withhold_stage(int stage) {
         g_last_cuda_error = cudaGetLastError();
         return W4_ERR_CUDA;
     }
+    withheld_stage(current_device()).store(v + 1, std::memory_order_relaxed);
     return W4_OK;
 }
 

@@ -149,7 +149,7 @@ w4_status launch_w8_tc(const W8Plan& p, const w4::W8Args& g, int32_t* part, bool
     if (ensure_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return W4_ERR_CUDA;
     const w4::W8TcArgs a = {g, part, p.tiles_m, p.tiles, static_cast<uint32_t>((1ull << 32) / p.tiles_m + 1),
                             p.grid_pairs % p.tiles_m, p.grid_pairs / p.tiles_m, p.F, p.chunks, p.cut_pairs, stages,
-                            early ? 1 : 0};
+                            early ? 1 : 0, withheld_stage(current_device()).load(std::memory_order_relaxed) - 1};
     launch_pdl(fn, dim3(2 * p.grid_pairs), dim3(w4::kW8Threads), smem, st, wmap, amap, a);
     const w4_status s = launch_status();
     if (s != W4_OK || p.ws == 0) return s;

@@ -58,6 +58,8 @@ struct W8TcArgs {
     int cut_pairs;       // pairs that share the tiles from F on
     int stages;
     int early;           // the kernel before does not write the weights
+    int withhold;        // a test's tile before which the producers stop, or -1 (a test for every stage
+                         // took 0.9 us of 33 x 28672 x 4096)
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -279,8 +281,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
             }
         }
         pdl_wait();
-        int n = 0;
-        while (ok && walk.next(a, pair, pairs, &u)) {
+        int n = 0, units = 0;
+        while (ok && walk.next(a, pair, pairs, &u) && units++ != a.withhold) {
             const int m0 = u.mt * TN + static_cast<int>(rank) * (TN / 2);
             const int o0 = u.ot * kW8Rows + static_cast<int>(rank) * 128;
             for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
@@ -332,7 +334,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8Threads, 1)
                         phase ^= 1u;
                     }
                 }
-                // also tracks any MMA issued before an abort
+                // An unfinished tile is not handed on: the other CTA's epilogue does not see
+                // this one's abort flag and would store it.  Its wait runs out as this one did.
+                if (!ok) break;
                 umma_commit_pair_elected(smem_u32(&acc_full[buf]));
                 ++i;
             }

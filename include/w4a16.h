@@ -323,7 +323,8 @@ const char *w4_status_string(int status);
  * current device.  Kernels whose waits are bounded set it instead of
  * hanging (codes 1..4: which wait gave up); the column gather / scatter set
  * code 5 for an index out of range; *code receives 0 when nothing was
- * recorded.  Synchronizes the device.  Returns W4_ERR_INVALID_ARG for code 5,
+ * recorded.  What a call that gave up left in its outputs is undefined.
+ * Synchronizes the device.  Returns W4_ERR_INVALID_ARG for code 5,
  * W4_ERR_TIMEOUT for the other non-zero codes, W4_ERR_CUDA on a CUDA
  * failure, W4_OK otherwise.
  */
@@ -398,8 +399,9 @@ w4_status w4_set_debug_checks(int on);
  * wait may last before the kernel gives up (0 restores the default, 2 s).
  * w4_debug_withhold_stage makes the producer of every CTA of the GEMV
  * kernels skip the copy of its stage number `stage` (-1: none, the default)
- * without issuing it, so the consumers' waits run out, the kernel unwinds,
- * and w4_device_error reports W4_ERR_TIMEOUT.  Nothing is left in flight and
+ * without issuing it, and those of the 8-bit product's tensor-core kernel
+ * stop before their tile number `stage`, so the consumers' waits run out,
+ * the kernel unwinds, and w4_device_error reports W4_ERR_TIMEOUT.  Nothing is left in flight and
  * the context stays usable.  For tests only.
  */
 w4_status w4_debug_set_wait_limit(unsigned long long ns);
