@@ -6,6 +6,9 @@ namespace {
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
+// Scales that the kernels read or write one at a time: part of a batch's or of the channels' may begin anywhere.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 w4_status check_w8(int M, int N, int K, long long ldw, int transposed, const void* W, const void* bias,
                    const void* Y) {
     if (M <= 0 || N <= 0 || K <= 0 || ldw < K || !W || !Y) return W4_ERR_INVALID_ARG;
@@ -221,7 +224,7 @@ w4_status w8_quantize_rows(const void* X, int R, int C, const float* channel_sca
                            float* scales, void* stream) {
     if (R <= 0 || C <= 0 || ld < C || !X || !codes || !scales) return W4_ERR_INVALID_ARG;
     if (std::max(R, C) > (1 << 30)) return W4_ERR_UNSUPPORTED;
-    if (!aligned16(X) || !aligned16(codes) || !aligned16(scales) || !aligned16(channel_scales) || ld % 16 != 0)
+    if (!aligned16(X) || !aligned16(codes) || !aligned4(scales) || !aligned16(channel_scales) || ld % 16 != 0)
         return W4_ERR_ALIGNMENT;
     return run_quantize_rows(static_cast<const uint16_t*>(X), R, C, channel_scales, codes, ld, scales,
                              static_cast<cudaStream_t>(stream));
@@ -246,7 +249,7 @@ w4_status w8a8_gemm(const int8_t* A, long long lda, const float* a_scales, int M
     if (s != W4_OK && s != W4_ERR_ALIGNMENT) return s;
     if (!A || !a_scales || lda < (transposed ? N : K) || (w_scales == nullptr) != (transposed != 0))
         return W4_ERR_INVALID_ARG;
-    if (s != W4_OK || !aligned16(A) || !aligned16(a_scales) || !aligned16(w_scales) || lda % 16 != 0)
+    if (s != W4_OK || !aligned16(A) || !aligned4(a_scales) || !aligned4(w_scales) || lda % 16 != 0)
         return W4_ERR_ALIGNMENT;
     const size_t need = w8a8_workspace_bytes(M, N, K, transposed);
     if (workspace_bytes < need || (need > 0 && !workspace)) return W4_ERR_WORKSPACE;

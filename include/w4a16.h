@@ -227,7 +227,8 @@ w4_status w4_invert_permutation(const int32_t *perm, int n, int32_t *inv, void *
  * (rows = channels), on tokens, and, with channel_scales = the weights' scales,
  * on the gradients dY of the transposed product.
  * Validation: R, C > 0; ld >= C; X, codes, scales non-NULL (W4_ERR_INVALID_ARG);
- * R, C at most 2^30 (W4_ERR_UNSUPPORTED); pointers 16-byte aligned and ld a multiple of 16 (W4_ERR_ALIGNMENT).
+ * R, C at most 2^30 (W4_ERR_UNSUPPORTED); X, channel_scales and codes 16-byte aligned, scales 4-byte, and ld a
+ * multiple of 16 (W4_ERR_ALIGNMENT).
  */
 w4_status w8_quantize_rows(const void *X, int R, int C, const float *channel_scales, int8_t *codes,
                            long long ld, float *scales, void *stream);
@@ -252,7 +253,9 @@ size_t w8a8_linear_workspace_bytes(int M, int N, int K, int transposed);
  * (bias may be NULL, w_scales as above); the length of the sum (K, transposed
  * N) at most 131071, beyond which int32 could overflow, and M, N, K at most
  * 2^30 (W4_ERR_UNSUPPORTED);
- * pointers 16-byte aligned, lda and ldw multiples of 16 (W4_ERR_ALIGNMENT);
+ * A, W, bias, Y and workspace 16-byte aligned, the scales 4-byte (part of a
+ * batch or of the channels may be taken), lda and ldw multiples of 16
+ * (W4_ERR_ALIGNMENT);
  * workspace_bytes >= w8a8_workspace_bytes (W4_ERR_WORKSPACE).
  */
 w4_status w8a8_gemm(const int8_t *A, long long lda, const float *a_scales, int M, int N, int K,
@@ -263,7 +266,8 @@ w4_status w8a8_gemm(const int8_t *A, long long lda, const float *a_scales, int M
  * w8a8_linear -- w8_quantize_rows on bf16 A and w8a8_gemm on its codes in one
  * call: Y = A . dequant(W)^T (A [M, K]) or, transposed, dX = A . dequant(W)
  * (A = dY [M, N]; w_scales is folded into the rows before they are quantized).
- * w_scales is needed in both directions.  Validation as for w8a8_gemm.
+ * w_scales is needed in both directions.  Validation as for w8a8_gemm, but
+ * w_scales is 16-byte aligned, as w8_quantize_rows takes it.
  */
 w4_status w8a8_linear(const void *A, int M, int N, int K, const int8_t *W, long long ldw,
                       const float *w_scales, const void *bias, int transposed, void *Y, void *workspace,
