@@ -176,10 +176,15 @@ struct NormGradArgs {
     float alpha, off;
 };
 
-// Blocks an SM holds: 512 threads' worth at two groups (128 registers each),
-// 1024 at one (64; with 768 of 80, 8192 x 1024 took 44 us instead of 39).
-__host__ __device__ constexpr int norm_grad_blocks_per_sm(int T, int G) {
-    return T == 1024 ? 1 : G == 2 ? 512 / T : 1024 / T;
+// Blocks an SM holds: 512 threads' worth at two groups (128 registers each)
+// and in rows of words, 1024 at one group of whole 16 bytes (64; with 768 of 80,
+// 8192 x 1024 took 44 us instead of 39).  Words need more registers for their
+// columns: with 1024 threads they spilled 136 bytes each way (513 x 2047 13.7 us
+// against 12.2, 300 x 1001 11.2 against 7.9, 4096 x 2047 with token gates 64.5
+// against 57.3); with 768 they spill 24, which is better for some (8192 x 2047
+// 97.9 against 105.7) and worse for others (4096 x 2047 73.2, 513 x 2047 13.9).
+__host__ __device__ constexpr int norm_grad_blocks_per_sm(int T, int G, int VEC) {
+    return T == 1024 ? 1 : G == 2 || VEC == 2 ? 512 / T : 1024 / T;
 }
 
 // One block takes rows blockIdx.x, + gridDim.x, ...; a thread keeps the same
@@ -188,7 +193,7 @@ __host__ __device__ constexpr int norm_grad_blocks_per_sm(int T, int G) {
 // where 1024 threads leave no room for them.  What a reduction separates is
 // read again from the pipe instead of being held.
 template <int T, int G, int VEC, bool ACC_SMEM>
-__global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G)) block_norm_backward_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(T, norm_grad_blocks_per_sm(T, G, VEC)) block_norm_backward_kernel(const NormGradArgs a) {
     using S = RowSpan<T, G, VEC>;
     constexpr bool PIPED = !ACC_SMEM;
     constexpr int kRegs = ACC_SMEM ? 1 : G;

@@ -28,7 +28,7 @@ struct NormLaunch {
 template <int T, int G, int VEC>
 struct NormGradBlocks {
     static int run(int M, int sms) {
-        return row_grid(M, sms * w4::norm_grad_blocks_per_sm(T, G));
+        return row_grid(M, sms * w4::norm_grad_blocks_per_sm(T, G, VEC));
     }
 };
 int norm_grad_blocks(int M, int C, int sms) { return dispatch_row<NormGradBlocks>(C, M, sms); }
