@@ -419,6 +419,36 @@ def w4_scatter_columns(A, idx, dst_cols: int, out=None):
 # tensors.  An ordinary call is made by the native module (binding/
 # w8_native.cpp) in one C function; where that finds an argument it does not
 # take (None), the call goes through the checks here, which say what is wrong.
+class _NoNative:
+    """In place of the native module where it cannot be had: takes no call, so the Python checks make
+    each of them, on the same kernels."""
+    @staticmethod
+    def _none(*args):
+        return None
+
+    quantize_rows = gemm = linear = norm = norm_backward = _none
+
+
+def _load_native():
+    import importlib.machinery
+    import importlib.util
+    import subprocess
+    import warnings
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("w8_native", _build.build_binding())
+        native = importlib.util.module_from_spec(importlib.util.spec_from_loader("w8_native", loader))
+        loader.exec_module(native)
+    except (OSError, ImportError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"the binding's native part could not be built or loaded ({e}); calls of the 8-bit layer and "
+                      "of the block norms go through Python and take a few microseconds more", RuntimeWarning)
+        return _NoNative
+    lib = library()
+    native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "w8_quantize_rows", "w8a8_workspace_bytes", "w8a8_linear_workspace_bytes", "w8a8_gemm", "w8a8_linear",
+        "w4_block_norm", "w4_block_norm_workspace_bytes", "w4_block_norm_backward")), BlockNorm, BlockNormGrad)
+    return native
+
+
 class _Torch:
     """torch, what the calls below use of it, and the native calls, looked up once."""
     torch = None
@@ -427,16 +457,7 @@ class _Torch:
     @classmethod
     def load(cls):
         torch = _torch()
-        import importlib.machinery
-        import importlib.util
-        loader = importlib.machinery.ExtensionFileLoader("w8_native", _build.build_binding())
-        native = importlib.util.module_from_spec(importlib.util.spec_from_loader("w8_native", loader))
-        loader.exec_module(native)
-        lib = library()
-        native.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-            "w8_quantize_rows", "w8a8_workspace_bytes", "w8a8_linear_workspace_bytes", "w8a8_gemm", "w8a8_linear",
-            "w4_block_norm", "w4_block_norm_workspace_bytes", "w4_block_norm_backward")), BlockNorm, BlockNormGrad)
-        cls.native = native
+        cls.native = _load_native()
         cls.bf16, cls.f32, cls.i8, cls.u8 = torch.bfloat16, torch.float32, torch.int8, torch.uint8
         cls.empty_like = torch.empty_like
         cls.get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
