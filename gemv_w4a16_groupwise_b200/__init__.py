@@ -451,11 +451,18 @@ def _load_native():
 
 class _Torch:
     """torch, what the calls below use of it, and the native calls, looked up once."""
-    torch = None
+    lock = threading.Lock()      # not the library's, which is taken inside
+    torch = None                 # set last: what reads it without the lock finds the rest
     native = None
 
     @classmethod
     def load(cls):
+        with cls.lock:
+            if cls.torch is None:
+                cls._load()
+
+    @classmethod
+    def _load(cls):
         torch = _torch()
         cls.native = _load_native()
         cls.bf16, cls.f32, cls.i8, cls.u8 = torch.bfloat16, torch.float32, torch.int8, torch.uint8
