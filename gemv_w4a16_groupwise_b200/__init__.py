@@ -599,13 +599,13 @@ def _w8_operands(A, dev, codes, scales, bias, transposed, out):
     return M, N, K, ldw, out
 
 
-def _w8_workspace(query, dev, M, N, K, transposed, like):
+def _scratch(query, dev, like, *shape):
     """Scratch of the size that the library asks for (a pure function of the shape and the device)."""
-    key = (query, dev, M, N, K, transposed)
+    key = (query, dev, *shape)
     n = _ws_cache.get(key)
     if n is None:
         with _OnDevice(dev):
-            n = int(getattr(_Torch.lib, query)(M, N, K, transposed))
+            n = int(getattr(_Torch.lib, query)(*shape))
         if len(_ws_cache) > 4096:
             _ws_cache.clear()
         _ws_cache[key] = n
@@ -636,7 +636,7 @@ def w8a8_gemm(A, a_scales, codes, scales=None, *, bias=None, transposed: bool = 
     lda = _check_codes(A, "A", dev)
     M, N, K, ldw, out = _w8_operands(A, dev, codes, scales, bias, tr, out)
     _check_rows(a_scales, "a_scales", _Torch.f32, dev, (M,))
-    ws, nws = _w8_workspace("w8a8_workspace_bytes", dev, M, N, K, tr, out)
+    ws, nws = _scratch("w8a8_workspace_bytes", dev, out, M, N, K, tr)
     _call("w8a8_gemm", dev, A.data_ptr(), lda, a_scales.data_ptr(), M, N, K, codes.data_ptr(), ldw, _ptr(scales),
           _ptr(bias), tr, out.data_ptr(), _ptr(ws), nws)
     return out
@@ -656,7 +656,7 @@ def w8a8_linear(A, codes, scales, *, bias=None, transposed: bool = False, out=No
         raise ValueError("scales of the weights are needed")
     tr = 1 if transposed else 0
     M, N, K, ldw, out = _w8_operands(A, dev, codes, scales, bias, tr, out)
-    ws, nws = _w8_workspace("w8a8_linear_workspace_bytes", dev, M, N, K, tr, out)
+    ws, nws = _scratch("w8a8_linear_workspace_bytes", dev, out, M, N, K, tr)
     _call("w8a8_linear", dev, A.data_ptr(), M, N, K, codes.data_ptr(), ldw, scales.data_ptr(), _ptr(bias), tr,
           out.data_ptr(), _ptr(ws), nws)
     return out
@@ -768,15 +768,10 @@ def w4_block_norm_backward(d_normed, residual, rstd, y=None, *, d_residual=None,
     d_pre = empty_like(pre_weight)
     d_post = None if post_weight is None else empty_like(post_weight)
     d_gate = None if gate is None else empty_like(gate)
-    key = ("norm", dev, M, C)
-    nws = _ws_cache.get(key)
-    if nws is None:
-        with _OnDevice(dev):
-            nws = _ws_cache[key] = int(_Torch.lib.w4_block_norm_workspace_bytes(M, C))
-    ws = d_x.new_empty(nws, dtype=_Torch.u8)
+    ws, nws = _scratch("w4_block_norm_workspace_bytes", dev, d_x, M, C)
     _call("w4_block_norm_backward", dev, d_normed.data_ptr(), _ptr(d_residual), residual.data_ptr(), rstd.data_ptr(),
           _ptr(y), M, C, _ptr(post_weight), _ptr(gate), kind, residual_scale, pre_weight.data_ptr(), weight_offset,
-          d_x.data_ptr(), _ptr(d_y), d_pre.data_ptr(), _ptr(d_post), _ptr(d_gate), ws.data_ptr(), nws)
+          d_x.data_ptr(), _ptr(d_y), d_pre.data_ptr(), _ptr(d_post), _ptr(d_gate), _ptr(ws), nws)
     return BlockNormGrad(d_x, d_y, d_pre, d_post, d_gate)
 
 
