@@ -53,13 +53,20 @@ struct QuantizeLaunch {
     }
 };
 
+// More than 8192 values in whole 16 bytes: three or four groups a thread waste fewer of them than 1024
+// threads would.
+template <>
+struct QuantizeLaunch<1024, 2, 8> {
+    template <typename... Args>
+    static w4_status run(const uint16_t* X, int R, int C, Args... args) {
+        return C <= 12288 ? QuantizeLaunch<512, 3, 8>::run(X, R, C, args...)
+                          : QuantizeLaunch<512, 4, 8>::run(X, R, C, args...);
+    }
+};
+
 w4_status run_quantize_rows(const uint16_t* X, int R, int C, const float* channel, int8_t* codes, long long ld,
                             float* scales, cudaStream_t st) {
     const int sms = device_info(current_device()).sms;
-    // three or four groups a thread waste fewer of them than 1024 threads would
-    if (C > 8192 && C <= w4::kRowMaxC && C % 8 == 0)
-        return C <= 12288 ? QuantizeLaunch<512, 3, 8>::run(X, R, C, channel, codes, ld, scales, sms, st)
-                          : QuantizeLaunch<512, 4, 8>::run(X, R, C, channel, codes, ld, scales, sms, st);
     if (C <= w4::kRowMaxC) return dispatch_row<QuantizeLaunch>(C, X, R, C, channel, codes, ld, scales, sms, st);
     if (C % 8 == 0)
         launch_pdl(w4::quantize_long_rows_kernel<8>, dim3(R), dim3(1024), 0, st, X, C, channel, codes, ld, scales);
