@@ -146,12 +146,12 @@ __global__ void __launch_bounds__(T, 1024 / T) block_norm_kernel(const NormArgs 
         }
         if constexpr (CODES) {
             top = __uint_as_float(block_max_bits<T>(__float_as_uint(top), ubuf[turn]));
-            const RowCodes sc = row_codes(top);
+            const RowCodes sc = row_codes<false>(top);
             if (threadIdx.x == 0) a.scales[m] = row_scale(top);
 #pragma unroll
             for (int g = 0; g < G; ++g)
                 store_codes<VEC>(span, static_cast<int8_t*>(a.normed) + static_cast<size_t>(m) * a.ld, g, C,
-                                    codes8(n[g], sc));
+                                    codes8<false>(n[g], sc));
         }
     }
 }

@@ -220,8 +220,8 @@ w4_status w4_invert_permutation(const int32_t *perm, int n, int32_t *inv, void *
  * (fp32 [C], or NULL), as int8 codes with one scale per row:
  *     scales[r] = fp32(max|v| / 127),   codes = rint(127 v / max|v|)
  * symmetric, round half to even; for bf16 v the codes are those of the exact
- * quotient (products with channel_scales are rounded to fp32 first, and their
- * quotients to within 2^-23 of themselves before the rounding).  A row of
+ * quotient; products with channel_scales are fp32, and the codes of such a row
+ * those of fp32 arithmetic, rint(fp32(fp32(127 v) / max|v|)).  A row of
  * zeros has scale 0 and codes 0; a row with an infinity or a NaN has scale NaN
  * and codes 0, so that everything it takes part in is NaN.  Used on weights
  * (rows = channels), on tokens, and, with channel_scales = the weights' scales,
