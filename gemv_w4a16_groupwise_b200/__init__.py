@@ -712,7 +712,9 @@ def w4_block_norm(x, y=None, *, pre_weight, post_weight=None, gate=None, residua
     is the norm after that block, pre_weight the one before the next; weights are
     w + weight_offset.  gate: bf16 [C] or [M, C].  ``quantize`` gives the normed rows as
     int8 codes and scales for :func:`w8a8_gemm` instead of bf16.  ``keep_rstd`` keeps what
-    :func:`w4_block_norm_backward` needs.  ``residual_out`` may be x or y (in place)."""
+    :func:`w4_block_norm_backward` needs.  ``residual_out`` may be x or y (in place).
+    A row's result does not depend on the others; with an odd C its last bits may differ
+    between an even and an odd place (rows there begin at either half of a word)."""
     r = _native().norm(x, y, pre_weight, post_weight, gate, residual_scale, weight_offset, eps, quantize, keep_rstd,
                        residual_out)
     if r is not None:
@@ -748,7 +750,8 @@ def w4_block_norm_backward(d_normed, residual, rstd, y=None, *, d_residual=None,
     the residual and rstd that it returned (``keep_rstd=True``), its y, weights and gate.
 
     All bf16: d_x, d_y [M, C], d_pre_weight, d_post_weight [C], d_gate in the gate's shape.
-    Quantized rows count as the values they stand for.  The same inputs give the same bits."""
+    Quantized rows count as the values they stand for.  The same inputs give the same bits
+    (a row by itself those of its place, as in the forward pass)."""
     r = _native().norm_backward(d_normed, residual, rstd, d_residual, y, pre_weight, post_weight, gate, residual_scale,
                                 weight_offset)
     if r is not None:

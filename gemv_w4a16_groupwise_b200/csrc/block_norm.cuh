@@ -18,8 +18,9 @@
 // A row is read from device memory once; what a reduction separates stays in
 // registers as bf16 or is read again from shared memory.  Sums and statistics
 // are fp32 in a fixed order.  Measured on 4096 x 4096 with a post norm and a
-// gate per token: forward 28.2 us (5.9 TB/s, bound by memory), backward 56 us
-// (4.8 TB/s, bound by issue slots and the latency of a row's reductions).
+// gate per token: forward 28.5 us (5.9 TB/s, bound by memory), backward with its
+// column sums 56.5 us (4.8 TB/s, bound by issue slots and the latency of a row's
+// reductions; 53.0 and 7.5 when the second kernel starts after the first).
 #pragma once
 
 #include "rows.cuh"

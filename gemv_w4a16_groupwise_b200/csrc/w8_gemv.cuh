@@ -2,16 +2,19 @@
 //
 // Bound by the weights' bytes, so the kernel is a stream with little in its
 // way: a block takes 16 weight rows at a time, its 8 warps interleaved 64-byte
-// pieces of them, and every lane has 16 loads of 16 bytes under way (two blocks
-// of an SM: 128 KB in flight): the next ones are asked for as soon as the
+// pieces of them, and every lane has 16 loads of 16 bytes under way (64 KB a
+// block, at most two blocks an SM): the next ones are asked for as soon as the
 // products have taken the last, before the sums of a finished 16 rows are
 // added up.  The loads land where
 // mma.sync.m16n8k32 wants them: lane (g, t) holds bytes 16 t .. 16 t + 15 of a
 // piece of rows g and g + 8, and of token g; that the four words stand for
 // other k than the instruction's own order is the same on both sides.  The
 // integer sums of the warps are added in shared memory.  1 x 28672 x 4096 in
-// 20.6 us (5.7 TB/s), 1 x 6144 x 4096 in 7.5 us; four blocks with half the loads
-// each take 28 and 9.8.
+// 20.4 us (5.8 TB/s), 1 x 6144 x 4096 in 7.5 us; four blocks with half the loads
+// each take 28 and 9.8.  Every block takes the same number of 16-row blocks, so
+// the grid does not always fill the SMs: 28672 outputs are 256 blocks of 7 (40 of
+// 148 SMs hold one), 6144 are 192 of 2 (104 hold one, with 64 KB in flight), and
+// that is what bounds the second.
 //
 // MT > 0: bf16 tokens, quantized by every block for itself while its first
 // weights are on their way (up to 16384 values a block, from L2): one launch

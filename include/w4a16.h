@@ -289,7 +289,10 @@ w4_status w8a8_linear(const void *A, int M, int N, int K, const int8_t *W, long 
  * (0 without one) and of the norm before the next, which the backward pass
  * takes.  residual may be x or y (in place).
  *   gate_kind: W4_GATE_NONE, W4_GATE_CHANNEL (bf16 [C]), W4_GATE_TOKEN (bf16 [M, C]).
- * All rows are bf16, dense.  Statistics are fp32.
+ * All rows are bf16, dense.  Statistics are fp32, added up in an order that
+ * depends on C alone, but for odd C also on whether the row's number is odd (such
+ * rows begin in the middle of a word): the same row may there differ in the last
+ * bits between an even and an odd place.  Other rows have no influence.
  * Validation: M, C > 0; C <= 16384, M <= 2^30 (W4_ERR_UNSUPPORTED); gate_kind in range;
  * eps > 0 and finite; x, pre_weight, normed non-NULL; residual non-NULL exactly
  * when y is; with scales ld >= C; pointers (and ld) 16-byte aligned.
