@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
         top = 0;
 #pragma unroll
         for (int w = 0; w < kT / 32; ++w) top = max(top, tops[m * (kT / 32) + w]);
-        const RowCodes sc = row_codes<false>(__uint_as_float(top));
+        const RowCodes sc = row_codes<true>(__uint_as_float(top));
         if (i0 == 0) token_scale[m] = row_scale(__uint_as_float(top));
         // codes, and zeros up to the end of the block's last step
 #pragma unroll
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kGvWarps * 32, 2) w8_gemv_kernel(const W8GemvA
             if (k < tb - 64) {
                 const uint4 x = raw[v * kGvWarps * 32 + threadIdx.x];
                 float2 f[4] = {unpack_bf16x2(x.x), unpack_bf16x2(x.y), unpack_bf16x2(x.z), unpack_bf16x2(x.w)};
-                *reinterpret_cast<uint2*>(tokens + m * tb + k) = codes8<false>(f, sc);
+                *reinterpret_cast<uint2*>(tokens + m * tb + k) = codes8<true>(f, sc);
             }
         }
         __syncthreads();

@@ -6,11 +6,11 @@
 //
 // No value is divided by the hardware's division: an IEEE division in every
 // thread of a row's block, and the scale's, cost more issue slots than the row's
-// own values.
+// own values.  How the quotient is had instead depends on the values.
 //
-// bf16 rows and normed rows: the code is rint(v inv), one fma, with inv the least
-// fp32 number that is not below 127 / max |v|, so above it by less than 2^-23 of
-// it.  For bf16 v this is the exact quotient rounded half to even.  Write
+// bf16 rows: the code is rint(v inv), one fma, with inv the least fp32 number
+// that is not below 127 / max |v|, so above it by less than 2^-23 of it.  This
+// is the exact quotient rounded half to even.  Write
 // v = i 2^-d and max |v| = b in units of the maximum's last place, b in
 // [128, 255], |i| <= 255: the quotient is 127 i 2^-d / b, and its distance from
 // a rounding border h + 1/2 is a multiple of 1 / (2^(d+1) b), at least 2^-(d+9)
@@ -22,19 +22,18 @@
 // what its product with the maximum leaves of 127 (one Newton step, which
 // leaves the rounding alone), and moved up by one where that is still positive.
 //
-// Normed rows are themselves off by more than that; 3e-6 of their codes lie beside
-// the exact quotients', as they do with a division in fp32, which took 14.7 us
-// instead of 14.0 for 2048 x 4096.
-//
-// Rows times channel factors (DIVIDED): quotients lie as close to a border as one
-// likes, and many lie on one but for a rounding: the scales of quantized bf16
-// weights are bf16 values over 127, which makes 2e-5 of the quotients of dY times
-// them ties.  The code is rint of the quotient that fp32 arithmetic gives, 127 v
-// rounded, divided by max |v| and rounded.  The division is the product with the
-// reciprocal and one correction by what that leaves (Markstein 1990: the quotient
-// as it should be rounded).  rint(v inv) takes four operations less for a pair of
-// values, 16.8 instead of 17.4 us for 2048 x 11008, but puts a third more of the
-// codes beside the exact ones.
+// fp32 rows (products with channel factors, normed rows): quotients lie as close
+// to a border as one likes, and many lie on one but for a rounding: both kinds of
+// row are products of two bf16 values but for a factor that cancels (the scales of
+// quantized bf16 weights are bf16 values over 127), so ties are common.  The code
+// is rint of the quotient that fp32 arithmetic gives, 127 v rounded, divided by
+// max |v| and rounded.  The division is the product with the reciprocal and one
+// correction by what that leaves (Markstein 1990: the quotient as it should be
+// rounded).  rint(v inv) takes four operations less for a pair of values, 16.8
+// instead of 17.4 us for 2048 x 11008 with factors and 14.0 instead of 14.7 for the
+// norm's codes of 2048 x 4096, but puts half as many codes again beside the exact
+// ones (3.1e-5 of dY times scales against 2.2e-5, 4.7e-6 of normed rows against
+// 2.9e-6).
 #pragma once
 
 #include "rows.cuh"
@@ -43,12 +42,13 @@ namespace w4 {
 
 // What turns a row's values into codes.
 struct RowCodes {
-    float inv;     // codes per unit of v pre; DIVIDED: 1 / top
+    float inv;     // bf16 rows: codes per unit of v pre; fp32 rows: 1 / top
     float top;     // max |v| pre
     float pre;     // 1, a power of two that keeps inv normal for extreme rows, or 0 for a poisoned row
 };
 
-template <bool DIVIDED>
+// BF16: the rows' values are bf16's.
+template <bool BF16>
 __device__ __forceinline__ RowCodes row_codes(float top) {
     RowCodes s;
     s.pre = 1.0f;
@@ -64,13 +64,13 @@ __device__ __forceinline__ RowCodes row_codes(float top) {
     s.top = top;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(top));
-    if constexpr (DIVIDED) {
-        s.inv = fmaf(fmaf(-r, top, 1.0f), r, r);
-    } else {
+    if constexpr (BF16) {
         float i = 127.0f * r;
         i = fmaf(fmaf(-i, top, 127.0f), r, i);
         // the sign of 127 - i top survives its rounding
         s.inv = fmaf(-i, top, 127.0f) > 0.0f ? __uint_as_float(__float_as_uint(i) + 1u) : i;
+    } else {
+        s.inv = fmaf(fmaf(-r, top, 1.0f), r, r);
     }
     if (!(top > 0.0f)) s.inv = 0.0f;
     return s;
@@ -84,7 +84,7 @@ __device__ __forceinline__ float row_scale(float top) {
 // Eight values as codes: rint of the quotient is in the low byte after adding
 // 1.5 * 2^23, which leaves the integer, rounded half to even, in the low
 // mantissa bits.
-template <bool DIVIDED>
+template <bool BF16>
 __device__ __forceinline__ uint2 codes8(float2 (&v)[4], const RowCodes& s) {
     if (s.pre != 1.0f) {       // the whole row: extreme, or poisoned (0 times an infinity is not 0)
 #pragma unroll
@@ -94,11 +94,11 @@ __device__ __forceinline__ uint2 codes8(float2 (&v)[4], const RowCodes& s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float2 f;
-        if constexpr (DIVIDED) {
+        if constexpr (BF16) {
+            f = ffma2(v[i], both(s.inv), both(12582912.0f));
+        } else {
             const float2 a = fmul2(v[i], both(127.0f)), q = fmul2(a, both(s.inv));
             f = fadd2(ffma2(ffma2(q, both(-s.top), a), both(s.inv), q), both(12582912.0f));
-        } else {
-            f = ffma2(v[i], both(s.inv), both(12582912.0f));
         }
         w[i] = prmt(__float_as_uint(f.x), __float_as_uint(f.y), 0x0040u);
     }
@@ -223,13 +223,13 @@ __global__ void __launch_bounds__(T, CHANNEL && G > 2 ? 1 : THREADS / T) quantiz
             top = max(t << 16, t & 0xFFFF0000u);
         }
         top = block_max_bits<T>(top, buf[turn]);
-        const RowCodes sc = row_codes<CHANNEL>(__uint_as_float(top));
+        const RowCodes sc = row_codes<!CHANNEL>(__uint_as_float(top));
         if (threadIdx.x == 0) scales[m] = row_scale(__uint_as_float(top));
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float2(&u)[4] = v[CHANNEL ? g : 0];
             if constexpr (!CHANNEL) unpack8(u, x[g]);
-            store_codes<VEC>(span, codes + static_cast<size_t>(m) * ld, g, C, codes8<CHANNEL>(u, sc));
+            store_codes<VEC>(span, codes + static_cast<size_t>(m) * ld, g, C, codes8<!CHANNEL>(u, sc));
         }
     }
 }
@@ -265,14 +265,14 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint16_t
         for (int i = 0; i < 4; ++i) t = max_abs(t, v[i]);
     }
     t = __uint_as_float(block_max_bits<1024>(__float_as_uint(t), buf));
-    const RowCodes sc = channel ? row_codes<true>(t) : row_codes<false>(t);
+    const RowCodes sc = channel ? row_codes<false>(t) : row_codes<true>(t);
     if (threadIdx.x == 0) scales[m] = row_scale(t);
 #pragma unroll 2
     for (int c0 = 0; c0 <= C; c0 += 8192) {
         const RowSpan<1024, 1, VEC> span(m, C, c0);
         float2 v[4];
         values(span, v);
-        store_codes<VEC>(span, codes + m * ld, 0, C, channel ? codes8<true>(v, sc) : codes8<false>(v, sc));
+        store_codes<VEC>(span, codes + m * ld, 0, C, channel ? codes8<false>(v, sc) : codes8<true>(v, sc));
     }
 }
 

@@ -281,10 +281,10 @@ w4_status w8a8_linear(const void *A, int M, int N, int K, const int8_t *W, long 
  *     normed   = norm(residual) * (pre_weight + weight_offset)
  * post_weight (the norm after the block) and gate may be left out; `normed`
  * reads the residual as it is stored.  normed is bf16 [M, C], or, when `scales`
- * is given, int8 codes (row stride ld) with one scale per row, as those of
- * w8_quantize_rows but from the fp32 values, their quotients to within 2^-23 of
- * themselves before the rounding: the input of w8a8_gemm.  Without y (the first
- * block) post_weight, gate and residual must be NULL and x itself is normed.
+ * is given, int8 codes (row stride ld) with one scale per row, quantized from
+ * fp32 as rows with channel_scales are by w8_quantize_rows: the input of
+ * w8a8_gemm.  Without y (the first block) post_weight, gate and residual must be
+ * NULL and x itself is normed.
  * rstd: fp32 [2, M], or NULL: 1 / sqrt(mean + eps) of the norm after the block
  * (0 without one) and of the norm before the next, which the backward pass
  * takes.  residual may be x or y (in place).

@@ -1,10 +1,11 @@
-"""The codes of rows times channel factors are those of fp32 arithmetic; how near these and the codes of normed
-rows are to the exact quotients.
+"""The codes of fp32 rows (rows times channel factors, normed rows): those of fp32 arithmetic, and how near
+they are to the exact quotients.
 
-Bound.  With channel factors 127 v and its quotient by max |v| are rounded to fp32, half a step (2^-24) each, before
-the rounding to a whole number: |code - 127 v / max |v|| <= 0.5 + 127 (2^-23 + 2^-48).  Other rows are multiplied, in
-one fma, by inv, the least fp32 number that is not below 127 / max |v|, so above it by less than 2^-23 of it.  The
-quotients here are taken in 64 bits of the same fp32 values (127 * 2^-52 off at most)."""
+Bound.  127 v and its quotient by max |v| are rounded to fp32, half a step (2^-24) each, before the rounding to
+a whole number: |code - 127 v / max |v|| <= 0.5 + 127 (2^-23 + 2^-48).  The quotients here are taken in 64 bits
+of the same fp32 values (127 * 2^-52 off at most).
+
+bf16 rows multiply by inv, the least fp32 number that is not below 127 / max |v|."""
 import numpy as np
 import pytest
 import torch
@@ -42,12 +43,8 @@ def _exact(v):
     return v * 127 / v.abs().amax(1, keepdim=True)
 
 
-def _as_fp32(codes, v):
-    assert torch.equal(codes.float(), torch.round(v * 127 / v.abs().amax(1, keepdim=True)))
-    _near(codes, v)
-
-
 def _near(codes, v):
+    assert torch.equal(codes.float(), torch.round(v * 127 / v.abs().amax(1, keepdim=True)))
     off = (codes.double() - _exact(v)).abs()
     assert (off <= NEAR).all(), f"{int((off > NEAR).sum())} codes of {off.numel()}, the worst off by {off.max().item():.9f}"
 
@@ -61,7 +58,7 @@ def test_rows_times_channel_factors(cuda_device, R, C):
     X = torch.randn(R, C, generator=g, device=dev).to(torch.bfloat16)
     f = torch.rand(C, generator=g, device=dev) * 0.002 + 1e-4
     codes, _ = w4.w8_quantize_rows(X, channel_scales=f)
-    _as_fp32(codes, X.float() * f)
+    _near(codes, X.float() * f)
 
 
 @pytest.mark.gpu
@@ -85,7 +82,7 @@ def test_gradients_times_the_scales_of_quantized_weights(cuda_device, R, C):
     _, ws = w4.w8_quantize_rows((0.02 * torch.randn(C, 512, generator=g, device=dev)).to(torch.bfloat16))
     X = torch.randn(R, C, generator=g, device=dev).to(torch.bfloat16)
     codes, _ = w4.w8_quantize_rows(X, channel_scales=ws)
-    _as_fp32(codes, X.float() * ws)
+    _near(codes, X.float() * ws)
 
 
 @pytest.mark.gpu
@@ -105,7 +102,7 @@ def test_extreme_fp32_rows(cuda_device, C):
         fine = [0, 4, 5]
         v = (X.float() * f)[fine]
         power = 2.0 ** -round(torch.log2(v.abs().max()).item())      # exact, so that 127 v stays in range
-        _as_fp32(codes[fine], (v.double() * power).float())
+        _near(codes[fine], (v.double() * power).float())
         assert not codes[1:4].any() and scales[1] == 0 and torch.isnan(scales[2:4]).all()
 
 
@@ -123,7 +120,7 @@ def test_one_factor_for_all_channels(cuda_device, C):
     for factor in (0.3, 0.0123, 7.7e-5, 1.9):
         f = torch.full((C,), factor, device=dev)
         codes, _ = w4.w8_quantize_rows(X, channel_scales=f)
-        _as_fp32(codes, X.float() * f)
+        _near(codes, X.float() * f)
         assert (codes[:, 0] == 127).all()
     for factor in (1.0, 0.125, 2.0 ** -20):
         codes, s = w4.w8_quantize_rows(X, channel_scales=torch.full((C,), factor, device=dev))
