@@ -645,7 +645,9 @@ def w8a8_gemm(A, a_scales, codes, scales=None, *, bias=None, transposed: bool = 
 def w8a8_linear(A, codes, scales, *, bias=None, transposed: bool = False, out=None):
     """8-bit linear layer on bf16 rows: :func:`w8_quantize_rows` on A and
     :func:`w8a8_gemm` in one call.  Y = A . dequant(codes)^T (A [M, K]), or,
-    transposed, dX = A . dequant(codes) (A [M, N]).  ``out`` may not overlap the inputs."""
+    transposed, dX = A . dequant(codes) (A [M, N]).  ``out`` may not overlap the inputs.
+    ``scales`` start on 16 bytes here; those of the two calls may be slices that do not,
+    but for ``channel_scales``."""
     r = _native().linear(A, codes, scales, bias, transposed, out)
     if r is not None:
         if r.__class__ is int:
